@@ -149,9 +149,12 @@ struct RowDst {
 
 // MXFP8 row scales are grouped per 128-wide K step: the byte of row r, 32-block kb of an R-row
 // matrix sits at ((kb / 4) * R + r) * 4 + kb % 4 (R = srows).
+// `col_end`: the end of the columns this pass writes (the tensor's width, or the end of the gate half of
+// a gated kind's gradient).  A K step that it cuts is shared with the pass over the other half, so its
+// bytes are written one by one there.
 template <int FMT>
 __device__ __forceinline__ RowDst row_dst(const QOut& q, int64_t w, int64_t srows, int64_t row0,
-                                          int lr0, int64_t col, int lane) {
+                                          int lr0, int64_t col, int64_t col_end, int lane) {
   RowDst d;
   if constexpr (FMT == MGS_FMT_MXFP8) {
     const int64_t nkb = w >> 5, nks = (nkb + 3) >> 2, kb = col >> 5;
@@ -163,9 +166,11 @@ __device__ __forceinline__ RowDst row_dst(const QOut& q, int64_t w, int64_t srow
     d.spitch = 4;
     d.pad = kb == nkb - 1 ? (uint32_t)(nks * 4 - nkb) : 0u;
     d.sc_lane = ((lane >> 2) & 3) == 0;
-    // the workgroup's first column (chunk 0) starts a K step: always for a unary kind or the gate
-    // half, for the up half of a gated kind when its offset (the output width) is a multiple of 128
-    d.dword_mode = ((col - 8 * (lane >> 2)) & 127) == 0;
+    // the workgroup's first column (chunk 0) starts a K step (always for a unary kind or the gate
+    // half, for the up half of a gated kind when its offset, the output width, is a multiple of 128)
+    // that this pass writes whole or that ends the tensor
+    const int64_t c0 = col - 8 * (lane >> 2);
+    d.dword_mode = (c0 & 127) == 0 && (c0 + 128 <= col_end || col_end == w);
     d.sd_lane = (lane >> 2) == 0;
     const uint64_t sbyte = reinterpret_cast<uint64_t>(q.row_scales) + (uint64_t)(row0 * 4) + d.svo;
     d.sd_aligned = (sbyte & 15) == 0;
@@ -703,7 +708,7 @@ __global__ __launch_bounds__(256) void act_fwd_kernel(ActArgs aa, GroupTable gt,
   float y[8][8];
   fwd_tile_y<KIND, XF32>(aa, gt, pi, x, x_copy, width_in, wa, bp.lr0, bp.col, valid, p, y);
   if (out.row_data)
-    emit_row<FMT>(y, row_dst<FMT>(out, wa, gt.total_rows, pi.row0, bp.lr0, bp.col, bp.lane), bp.lr0, pi.nrows, valid, s_enc);
+    emit_row<FMT>(y, row_dst<FMT>(out, wa, gt.total_rows, pi.row0, bp.lr0, bp.col, wa, bp.lane), bp.lr0, pi.nrows, valid, s_enc);
   if (cs_part) {
     float cs[8];
 #pragma unroll
@@ -804,7 +809,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActArgs aa, GroupTable gt,
   float p[8];
   load_probs(probs, pi, gt.total_rows, lr0, p);
   const Bf16View dxv = bf16_view(dx, width_in, pi.row0, gt.total_rows, lr0, col);
-  const RowDst rd = row_dst<FMT>(dxq, width_in, gt.total_rows, pi.row0, lr0, col, bp.lane);
+  const RowDst rd = row_dst<FMT>(dxq, width_in, gt.total_rows, pi.row0, lr0, col, wa, bp.lane);
 
   // recompute first: y = a * p -> columnwise codes of the activation, one column of the lane's tile
   // at a time, so that the inputs (not 64 FP32 results) are what stays live into the dx phase; the
@@ -866,7 +871,7 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActArgs aa, GroupTable gt,
   if (dxq.col_data) stage_tile<FMT>(d, st_dx, bp, s_dx_col, dxq.col_rht);
   // gated: the up half in the same registers
   if constexpr (GATED) {
-    const RowDst ru = row_dst<FMT>(dxq, width_in, gt.total_rows, pi.row0, lr0, wa + col, bp.lane);
+    const RowDst ru = row_dst<FMT>(dxq, width_in, gt.total_rows, pi.row0, lr0, wa + col, width_in, bp.lane);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       launder(xg[i]);
