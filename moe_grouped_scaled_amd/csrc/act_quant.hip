@@ -617,8 +617,10 @@ __device__ __forceinline__ void stage_tile(const float (&y)[8][8], uint8_t* st, 
 // Write a staged block (after a barrier) to the group's columnwise tensor of width w: the data of
 // column cj at w * coff + cj * mp + 128 blk (elements), MXFP8 scales as the K-step dword of
 // (blk, cj), NVFP4 scales as 8 bytes at cj * mp / 16 + 8 blk.
+// `col_end`: the end of the columns staged here (columns past it are not written: behind the gate half of a
+// gated kind's gradient they are the up half's).
 template <int FMT>
-__device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int64_t w,
+__device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int64_t w, int64_t col_end,
                                           int64_t total_padded, const BlockPos& bp) {
   constexpr int P = Stage<FMT>::PITCH;
   const int64_t e0 = w * bp.pi.coff;
@@ -631,13 +633,13 @@ __device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int6
       const int idx = t + 256 * k, c = idx >> 3, ch = idx & 7;
       const uint2 a = *reinterpret_cast<const uint2*>(st + c * P + 16 * ch);
       const uint2 b = *reinterpret_cast<const uint2*>(st + c * P + 16 * ch + 8);
-      const bool ok = bp.col0 + c < w;
+      const bool ok = bp.col0 + c < col_end;
       bst16(make_uint4(a.x, a.y, b.x, b.y), dv, ok ? (uint32_t)(bp.col0 + c) * mp + 16u * ch : MASKED, 0);
     }
     const rsrc_t sv = view(q.col_scales, (e0 >> 5) + 4 * ((int64_t)bp.blk * w + bp.col0), (w * total_padded) >> 5);
     if (t < BLOCK_COLS) {
       const uint32_t d = *reinterpret_cast<const uint32_t*>(st + BLOCK_COLS * P + 4 * t);
-      bst4(d, sv, bp.col0 + t < w ? 4u * t : MASKED, 0);
+      bst4(d, sv, bp.col0 + t < col_end ? 4u * t : MASKED, 0);
     }
   } else {
     const rsrc_t dv = view(q.col_data, (e0 + 128 * (int64_t)bp.blk) >> 1, (w * total_padded) >> 1);
@@ -646,13 +648,13 @@ __device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int6
       const int idx = t + 256 * k, c = idx >> 2, ch = idx & 3;
       const uint2 a = *reinterpret_cast<const uint2*>(st + c * P + 16 * ch);
       const uint2 b = *reinterpret_cast<const uint2*>(st + c * P + 16 * ch + 8);
-      const bool ok = bp.col0 + c < w;
+      const bool ok = bp.col0 + c < col_end;
       bst16(make_uint4(a.x, a.y, b.x, b.y), dv, ok ? ((uint32_t)(bp.col0 + c) * mp >> 1) + 16u * ch : MASKED, 0);
     }
     const rsrc_t sv = view(q.col_scales, (e0 >> 4) + 8 * (int64_t)bp.blk, (w * total_padded) >> 4);
     if (t < BLOCK_COLS) {
       const uint2 d = *reinterpret_cast<const uint2*>(st + BLOCK_COLS * P + 8 * t);
-      bst8(d, sv, bp.col0 + t < w ? (uint32_t)(bp.col0 + t) * (mp >> 4) : MASKED, 0);
+      bst8(d, sv, bp.col0 + t < col_end ? (uint32_t)(bp.col0 + t) * (mp >> 4) : MASKED, 0);
     }
   }
 }
@@ -722,7 +724,7 @@ __global__ __launch_bounds__(256) void act_fwd_kernel(ActArgs aa, GroupTable gt,
   if (out.col_data) stage_tile<FMT>(y, stage, bp, s_enc_col, out.col_rht);
   if (out.col_data || cs_part) {
     __syncthreads();
-    if (out.col_data) flush_col<FMT>(stage, out, wa, (int64_t)PANEL_ROWS * gt.num_panels, bp);
+    if (out.col_data) flush_col<FMT>(stage, out, wa, wa, (int64_t)PANEL_ROWS * gt.num_panels, bp);
     if (cs_part) cs_flush(cs_lds, cs_part, wa, bp.col0, wa, 0, bp.gb);
   }
 }
@@ -931,14 +933,14 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActArgs aa, GroupTable gt,
       if constexpr (GATED) cs_flush(cs_lds + 4 * BLOCK_COLS, cs_part, width_in, bp.col0, wa, wa, bp.gb);
     }
     if (dxq.col_data) {
-      flush_col<FMT>(st_dx, dxq, width_in, total_padded, bp);
+      flush_col<FMT>(st_dx, dxq, width_in, wa, total_padded, bp);
       if constexpr (GATED) {
         BlockPos bu = bp;
         bu.col0 += wa;
-        flush_col<FMT>(st_up, dxq, width_in, total_padded, bu);
+        flush_col<FMT>(st_up, dxq, width_in, width_in, total_padded, bu);
       }
     }
-    if (actq.col_data) flush_col<FMT>(st_act, actq, wa, total_padded, bp);
+    if (actq.col_data) flush_col<FMT>(st_act, actq, wa, wa, total_padded, bp);
   }
 }
 
