@@ -1,6 +1,6 @@
 /*
  * mgs.h -- C ABI of the MI355X (gfx950) library for the fused MoE expert-MLP hot path:
- * per-row scaled activation + grouped block quantization (MXFP8 / NVFP4) + grouped MX GEMM.
+ * per-row scaled activation + grouped block quantization (MXFP8 / NVFP4 / MXFP4) + grouped MX GEMM.
  *
  * Sources (web pages the method is described on):
  *   [P1] "[PyTorch] Enable fused activation recompute for ScaledTanhSReLU" (TransformerEngine PR 3473)
@@ -23,7 +23,7 @@
  *   - Quantized widths (the quantized, contiguous dimension) must be multiples of 32, at most 2^24.
  *   - Size limits of the quantizing entry points (MGS_ERR_SHAPE beyond them): one group's columnwise
  *     matrix, roundup(m_g, 128) x W elements, stays below 2^31, and so does the byte size of the
- *     rowwise MXFP8 scale array, 4 * M * ceil(W / 128).
+ *     rowwise MXFP8 / MXFP4 scale array, 4 * M * ceil(W / 128).
  *   - Arithmetic follows IEEE FP32 with round-to-nearest-even; results are deterministic (no float
  *     atomics, fixed reduction orders).
  *
@@ -37,12 +37,19 @@
  *     colwise : group g at data + W*coff[g]/2:      data [W, mp_g/2]
  *               group g at scales + W*coff[g]/16:   scales [W, mp_g/16]   group_scale f32 [E]
  *   where mp_g = roundup(m_g, 128) and coff[g] = sum_{h<g} mp_h; padding tokens are written as zeros.
- *   "K-step grouped" MXFP8 scales of an [R x K] matrix keep the four 32-block scales of each
+ *   MXFP4 (E2M1 elements two per byte as NVFP4's, E8M0 scale per 32, no group scale):
+ *     rowwise : data u8 [M, W/2]                    scales: K-step grouped over [M, W]
+ *     colwise : group g at data + W*coff[g]/2:      data [W, mp_g/2]
+ *               group g at scales + W*coff[g]/32:   scales: K-step grouped over [W, mp_g]
+ *   "K-step grouped" MXFP8 and MXFP4 scales of an [R x K] matrix keep the four 32-block scales of each
  *   128-wide K step together per row, steps outermost: the scale of (row r, block kb) is the byte
  *   ((kb / 4) * R + r) * 4 + kb % 4; 4 * R * ceil(K / 128) bytes, unused bytes of a partial last
  *   step zero.  (One aligned dword per row and K step: what the grouped GEMM stages per step.)
  *   MXFP8 scale of a block with maximum magnitude amax: E8M0 code clamp(floor(log2 amax) - 8 + 127, 0, 254)
  *   (0 for an all-zero block), element = E4M3(y / 2^(code-127)) rounded to nearest-even, saturated at 448.
+ *   MXFP4 scale of a block: E8M0 code clamp(floor(log2 amax) - 2 + 127, 0, 254) (0 for an all-zero
+ *     block), element = E2M1(y / 2^(code-127)) rounded to nearest-even, saturated at 6 (the OCP
+ *     microscaling rule: the largest E2M1 exponent is 2).  Finite inputs.
  *   NVFP4 (per group g, FP32): S_enc = 2688 / amax_g (1 if amax_g == 0, FLT_MAX on overflow);
  *   block scale s_b = E4M3((amax_b / 6) * S_enc); element = E2M1(y * (S_enc / s_b)) (0 if s_b == 0);
  *   group_scale[g] = S_dec = 1 / S_enc; dequantized value = e2m1 * s_b * S_dec.
@@ -96,7 +103,7 @@ typedef enum {
   MGS_ACT_GLU = 7
 } mgs_act_kind;
 
-typedef enum { MGS_FMT_MXFP8 = 0, MGS_FMT_NVFP4 = 1 } mgs_fmt;
+typedef enum { MGS_FMT_MXFP8 = 0, MGS_FMT_NVFP4 = 1, MGS_FMT_MXFP4 = 2 } mgs_fmt;
 
 typedef enum { MGS_DTYPE_BF16 = 0, MGS_DTYPE_F32 = 1 } mgs_dtype;
 

@@ -20,7 +20,7 @@ ERRORS = {-1: "MGS_ERR_INVALID_ARG", -2: "MGS_ERR_SHAPE", -3: "MGS_ERR_UNSUPPORT
 
 ACT = {"identity": 0, "srelu": 1, "tanh_srelu": 2, "swiglu": 3, "clamped_swiglu": 4, "gelu": 5, "sigmoid": 6,
        "glu": 7}
-FMT = {"mxfp8": 0, "nvfp4": 1}
+FMT = {"mxfp8": 0, "nvfp4": 1, "mxfp4": 2}
 GEMM_MODE = {"fprop": 0, "dgrad": 1, "wgrad": 2}
 DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 NBYTES = {"data": 0, "scales": 1, "group_scale": 2}

@@ -18,6 +18,8 @@
 // wave); rowwise codes go out as 8-byte stores (128 contiguous bytes per row and wave), columnwise
 // codes as 8-byte stores (32 contiguous token bytes per column and panel).  Consecutive panels of a
 // column tile are placed on the same XCD so the columnwise lines they share are merged in one L2.
+#include <type_traits>
+
 #include "mgs_device.h"
 
 namespace mgs {
@@ -149,6 +151,14 @@ struct RowDst {
 
 // MXFP8 row scales are grouped per 128-wide K step: the byte of row r, 32-block kb of an R-row
 // matrix sits at ((kb / 4) * R + r) * 4 + kb % 4 (R = srows).
+//
+// The formats with E8M0 scales per 32 elements (MXFP8, MXFP4) share that layout; MXFP4 and NVFP4
+// pack two codes per byte.
+template <int FMT>
+constexpr bool is_mx() { return FMT == MGS_FMT_MXFP8 || FMT == MGS_FMT_MXFP4; }
+template <int FMT>
+constexpr int per_byte() { return FMT == MGS_FMT_MXFP8 ? 1 : 2; }
+
 // `col_end`: the end of the columns this pass writes (the tensor's width, or the end of the gate half of
 // a gated kind's gradient).  A K step that it cuts is shared with the pass over the other half, so its
 // bytes are written one by one there.
@@ -156,12 +166,13 @@ template <int FMT>
 __device__ __forceinline__ RowDst row_dst(const QOut& q, int64_t w, int64_t srows, int64_t row0,
                                           int lr0, int64_t col, int64_t col_end, int lane) {
   RowDst d;
-  if constexpr (FMT == MGS_FMT_MXFP8) {
+  if constexpr (is_mx<FMT>()) {
+    constexpr int PB = per_byte<FMT>();
     const int64_t nkb = w >> 5, nks = (nkb + 3) >> 2, kb = col >> 5;
-    d.data = view(q.row_data, row0 * w, srows * w);
+    d.data = view(q.row_data, row0 * w / PB, srows * w / PB);
     d.scales = view(q.row_scales, row0 * 4, srows * 4 * nks);
-    d.dvo = (uint32_t)lr0 * (uint32_t)w + (uint32_t)col;
-    d.dpitch = (uint32_t)w;
+    d.dvo = ((uint32_t)lr0 * (uint32_t)w + (uint32_t)col) / PB;
+    d.dpitch = (uint32_t)w / PB;
     d.svo = (uint32_t)(kb >> 2) * (uint32_t)srows * 4u + (uint32_t)lr0 * 4u + (uint32_t)(kb & 3);
     d.spitch = 4;
     d.pad = kb == nkb - 1 ? (uint32_t)(nks * 4 - nkb) : 0u;
@@ -241,18 +252,26 @@ __device__ __forceinline__ uint32_t gather_scale_dword(uint32_t code) {
 
 // Rowwise quantization of row i (8 values) of the lane's tile; rv: the row is real, valid: the
 // lane's columns are.  MXFP8 in dword mode returns the row's scale dword (in the chunk-0 lanes) for
-// flush_row_scales; otherwise the lane stores its block's scale byte here.
+// flush_row_scales (MXFP4 alike); otherwise the lane stores its block's scale byte here.
 template <int FMT>
 __device__ __forceinline__ uint32_t quant_row(const float (&v)[8], const RowDst& d, int i, bool rv,
                                               bool valid, float s_enc) {
   float m = absmax8(v);
-  if constexpr (FMT == MGS_FMT_MXFP8) {
+  if constexpr (is_mx<FMT>()) {
     m = row4_max(m);
-    const Mx8 e = mx_encode8(v, m);
-    bst8(e.q, d.data, rv ? d.dvo : MASKED, i * d.dpitch);
-    if (d.dword_mode) return gather_scale_dword(valid ? e.code : 0u);
+    uint32_t code;
+    if constexpr (FMT == MGS_FMT_MXFP8) {
+      const Mx8 e = mx_encode8(v, m);
+      bst8(e.q, d.data, rv ? d.dvo : MASKED, i * d.dpitch);
+      code = e.code;
+    } else {
+      const Mx4 e = mx4_encode8(v, m);
+      bst4(e.q, d.data, rv ? d.dvo : MASKED, i * d.dpitch);
+      code = e.code;
+    }
+    if (d.dword_mode) return gather_scale_dword(valid ? code : 0u);
     const bool sv = rv && d.sc_lane;
-    bst1(e.code, d.scales, sv ? d.svo : MASKED, i * d.spitch);
+    bst1(code, d.scales, sv ? d.svo : MASKED, i * d.spitch);
 #pragma unroll
     for (uint32_t t = 1; t <= 3; ++t) bst1(0, d.scales, sv && t <= d.pad ? d.svo + t : MASKED, i * d.spitch);
     return 0u;
@@ -268,13 +287,13 @@ __device__ __forceinline__ uint32_t quant_row(const float (&v)[8], const RowDst&
   }
 }
 
-// MXFP8: the scale dwords of the tile's eight rows (rows lr0 .. lr0 + 7 of the panel, real when
+// MXFP8, MXFP4: the scale dwords of the tile's eight rows (rows lr0 .. lr0 + 7 of the panel, real when
 // < nrows) from the chunk-0 lanes: two 16-byte stores when all eight are real and aligned, else one
 // dword per real row.
 template <int FMT>
 __device__ __forceinline__ void flush_row_scales(const RowDst& d, const uint32_t (&sdw)[8], int lr0,
                                                  int nrows) {
-  if constexpr (FMT == MGS_FMT_MXFP8) {
+  if constexpr (is_mx<FMT>()) {
     if (!d.dword_mode || !d.sd_lane) return;
     if (d.sd_aligned && lr0 + 8 <= nrows) {
       bst16(make_uint4(sdw[0], sdw[1], sdw[2], sdw[3]), d.scales, d.svo, 0);
@@ -506,7 +525,7 @@ struct Stage {
   // bytes per staged column: the block's codes plus 8 bytes of padding, which spreads the lanes'
   // 8-byte writes of eight columns apart over four bank groups instead of one
   static constexpr int PITCH = FMT == MGS_FMT_MXFP8 ? 136 : 72;
-  static constexpr int SCALES = FMT == MGS_FMT_MXFP8 ? 4 : 8;  // scale bytes per column and block
+  static constexpr int SCALES = is_mx<FMT>() ? 4 : 8;  // scale bytes per column and block
   static constexpr int BYTES = BLOCK_COLS * (PITCH + SCALES);
 };
 
@@ -560,6 +579,11 @@ __device__ __forceinline__ void stage_col(const float (&v)[8], uint8_t* st, cons
     m = quad_max(m);
     const Mx8 e = mx_encode8(v, m);
     *reinterpret_cast<uint2*>(st + c * P + 32 * bp.wave + bp.lr0) = e.q;
+    if (bp.lr0 == 0) st[BLOCK_COLS * P + 4 * c + bp.wave] = (uint8_t)e.code;
+  } else if constexpr (FMT == MGS_FMT_MXFP4) {
+    m = quad_max(m);
+    const Mx4 e = mx4_encode8(v, m);
+    *reinterpret_cast<uint32_t*>(st + c * P + 16 * bp.wave + (bp.lr0 >> 1)) = e.q;
     if (bp.lr0 == 0) st[BLOCK_COLS * P + 4 * c + bp.wave] = (uint8_t)e.code;
   } else {
     m = pair1_max(m);
@@ -615,7 +639,7 @@ __device__ __forceinline__ void stage_tile(const float (&y)[8][8], uint8_t* st, 
 }
 
 // Write a staged block (after a barrier) to the group's columnwise tensor of width w: the data of
-// column cj at w * coff + cj * mp + 128 blk (elements), MXFP8 scales as the K-step dword of
+// column cj at w * coff + cj * mp + 128 blk (elements), MXFP8 and MXFP4 scales as the K-step dword of
 // (blk, cj), NVFP4 scales as 8 bytes at cj * mp / 16 + 8 blk.
 // `col_end`: the end of the columns staged here (columns past it are not written: behind the gate half of a
 // gated kind's gradient they are the up half's).
@@ -636,11 +660,6 @@ __device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int6
       const bool ok = bp.col0 + c < col_end;
       bst16(make_uint4(a.x, a.y, b.x, b.y), dv, ok ? (uint32_t)(bp.col0 + c) * mp + 16u * ch : MASKED, 0);
     }
-    const rsrc_t sv = view(q.col_scales, (e0 >> 5) + 4 * ((int64_t)bp.blk * w + bp.col0), (w * total_padded) >> 5);
-    if (t < BLOCK_COLS) {
-      const uint32_t d = *reinterpret_cast<const uint32_t*>(st + BLOCK_COLS * P + 4 * t);
-      bst4(d, sv, bp.col0 + t < col_end ? 4u * t : MASKED, 0);
-    }
   } else {
     const rsrc_t dv = view(q.col_data, (e0 + 128 * (int64_t)bp.blk) >> 1, (w * total_padded) >> 1);
 #pragma unroll
@@ -651,6 +670,14 @@ __device__ __forceinline__ void flush_col(const uint8_t* st, const QOut& q, int6
       const bool ok = bp.col0 + c < col_end;
       bst16(make_uint4(a.x, a.y, b.x, b.y), dv, ok ? ((uint32_t)(bp.col0 + c) * mp >> 1) + 16u * ch : MASKED, 0);
     }
+  }
+  if constexpr (is_mx<FMT>()) {
+    const rsrc_t sv = view(q.col_scales, (e0 >> 5) + 4 * ((int64_t)bp.blk * w + bp.col0), (w * total_padded) >> 5);
+    if (t < BLOCK_COLS) {
+      const uint32_t d = *reinterpret_cast<const uint32_t*>(st + BLOCK_COLS * P + 4 * t);
+      bst4(d, sv, bp.col0 + t < col_end ? 4u * t : MASKED, 0);
+    }
+  } else {
     const rsrc_t sv = view(q.col_scales, (e0 >> 4) + 8 * (int64_t)bp.blk, (w * total_padded) >> 4);
     if (t < BLOCK_COLS) {
       const uint2 d = *reinterpret_cast<const uint2*>(st + BLOCK_COLS * P + 8 * t);
@@ -1204,21 +1231,25 @@ void group_amax_dispatch(int kind, hipStream_t st, const ActArgs& aa, const Grou
   }
 }
 
+// Runs `f` with the format as a compile-time constant.
+template <typename F>
+void with_fmt(int fmt, F f) {
+  if (fmt == MGS_FMT_MXFP8) f(std::integral_constant<int, MGS_FMT_MXFP8>{});
+  else if (fmt == MGS_FMT_NVFP4) f(std::integral_constant<int, MGS_FMT_NVFP4>{});
+  else f(std::integral_constant<int, MGS_FMT_MXFP4>{});
+}
+
 template <int KIND, bool XF32>
 void fwd_dispatch_fmt(int fmt, dim3 grid, hipStream_t st, const ActArgs& aa, const GroupTable& gt,
                       const void* x, const float* probs, int64_t width_in, const QOut& out,
                       float* cs_part, int n_ct, uint16_t* x_copy) {
-  if (gt.dev) {
-    // device-resident split sizes: the offsets come from the device table
-    if (fmt == MGS_FMT_MXFP8)
-      hipLaunchKernelGGL((act_fwd_kernel<KIND, MGS_FMT_MXFP8, XF32, true>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
+  with_fmt(fmt, [&](auto f) {
+    constexpr int FMT = decltype(f)::value;
+    if (gt.dev)  // device-resident split sizes: the offsets come from the device table
+      hipLaunchKernelGGL((act_fwd_kernel<KIND, FMT, XF32, true>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
     else
-      hipLaunchKernelGGL((act_fwd_kernel<KIND, MGS_FMT_NVFP4, XF32, true>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
-  } else if (fmt == MGS_FMT_MXFP8) {
-    hipLaunchKernelGGL((act_fwd_kernel<KIND, MGS_FMT_MXFP8, XF32, false>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
-  } else {
-    hipLaunchKernelGGL((act_fwd_kernel<KIND, MGS_FMT_NVFP4, XF32, false>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
-  }
+      hipLaunchKernelGGL((act_fwd_kernel<KIND, FMT, XF32, false>), grid, dim3(256), 0, st, aa, gt, x, probs, width_in, out, cs_part, n_ct, x_copy);
+  });
 }
 
 template <int KIND>
@@ -1234,14 +1265,13 @@ void bwd_dispatch_fmt(int fmt, dim3 grid, hipStream_t st, const ActArgs& aa, con
                       const uint16_t* x, const uint16_t* dy, const float* probs, int64_t width_in,
                       int64_t wa, uint16_t* dx, const QOut& dxq, float* dp_part, float* cs_part,
                       const QOut& actq, int n_ct) {
-  if (gt.dev && fmt == MGS_FMT_MXFP8)  // device-resident split sizes
-    hipLaunchKernelGGL((act_bwd_kernel<KIND, MGS_FMT_MXFP8, true>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
-  else if (gt.dev)
-    hipLaunchKernelGGL((act_bwd_kernel<KIND, MGS_FMT_NVFP4, true>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
-  else if (fmt == MGS_FMT_MXFP8)
-    hipLaunchKernelGGL((act_bwd_kernel<KIND, MGS_FMT_MXFP8, false>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
-  else
-    hipLaunchKernelGGL((act_bwd_kernel<KIND, MGS_FMT_NVFP4, false>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
+  with_fmt(fmt, [&](auto f) {
+    constexpr int FMT = decltype(f)::value;
+    if (gt.dev)  // device-resident split sizes
+      hipLaunchKernelGGL((act_bwd_kernel<KIND, FMT, true>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
+    else
+      hipLaunchKernelGGL((act_bwd_kernel<KIND, FMT, false>), grid, dim3(256), 0, st, aa, gt, x, dy, probs, width_in, wa, dx, dxq, dp_part, cs_part, actq, n_ct);
+  });
 }
 
 // dprobs from its partials (when dprobs is non-null) and the column sums from theirs (when cs_out is

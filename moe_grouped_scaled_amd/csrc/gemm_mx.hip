@@ -39,7 +39,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int BK = 128;                  // K elements per step
 
 // One operand of a tile: `rows` valid rows starting at `data` (row stride `ld` bytes).  Scales:
-// MXFP8 keeps them grouped per 128-wide K step -- the byte of (row r, 32-block kb) of the scale
+// MXFP8 and MXFP4 keep them grouped per 128-wide K step -- the byte of (row r, 32-block kb) of the scale
 // matrix is at sbase[((kb / 4) * srows + srow0 + r) * 4 + kb % 4]; NVFP4 keeps them row-major with
 // `sld` bytes per row starting at sbase + srow0 * sld.
 struct Operand {
@@ -66,7 +66,7 @@ struct TileJob {
 
 constexpr int TILE_BLOCK_N = 4;
 
-// Operand layouts by mode (E groups, elements per byte 1 for MXFP8 and 2 for NVFP4):
+// Operand layouts by mode (E groups, elements per byte 1 for MXFP8, 2 for NVFP4 and MXFP4):
 //   FPROP / DGRAD A: rowwise qtensor [M x k]                 (scale matrix: all M rows)
 //   FPROP B:         rowwise qtensor [E * n x k]             (scale matrix: all E * n rows)
 //   DGRAD B:         columnwise qtensor of an [E * k x n] weight: per group [n x kp], kp = roundup(k, 128)
@@ -83,7 +83,7 @@ __device__ __forceinline__ TileJob make_job(const GemmArgs& ga, const Table& tt,
   j.g = g;
   const int lt = tile - tt.tile_off[g];
   const bool nv = ga.fmt == MGS_FMT_NVFP4;
-  const int ediv = nv ? 2 : 1;            // elements per byte
+  const int ediv = ga.fmt == MGS_FMT_MXFP8 ? 1 : 2;  // elements per byte
   const int sblk = nv ? 16 : 32;          // elements per scale
   // Tiles of a group run in column blocks of TILE_BLOCK_N tile columns, row-major inside a block:
   // the workgroups in flight on one XCD (dispatched together) then share each K slice of A with
@@ -1019,6 +1019,18 @@ void gemm_nvfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   epilogue_nv256(j, ga, acc, bias_lds, wm, wn, r32, h32);
 }
 
+// ------------------------------------------------------------------------------------ MXFP4 path
+
+// raw buffer view of `bytes` bytes at `p` for the compiler's buffer loads (p and bytes wave-uniform)
+typedef __amdgpu_buffer_rsrc_t fp4_view_t;
+__device__ __forceinline__ fp4_view_t fp4_view(const uint8_t* p, int64_t bytes) {
+  const sdesc_t d = gemm_view(p, bytes);
+  const uint64_t a = (uint64_t)(uint32_t)d[0] | ((uint64_t)(uint32_t)d[1] << 32);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a), 0, d[2], RSRC_WORD3);
+}
+
+#include "gemm_mxfp4.h"
+
 }  // namespace
 
 namespace {
@@ -1167,34 +1179,51 @@ __global__ __launch_bounds__(256) void gemm_table_kernel(const GroupTable* __res
 
 }  // namespace
 
+namespace {
+
+typedef void (*GemmKernel)(GemmArgs, GemmTable);
+
+// The kernel of a launch and its tile.
+struct GemmVariant {
+  GemmKernel kernel;
+  int tm, tn;
+};
+
+GemmVariant gemm_variant(const GemmArgs& ga, const GroupTable& gt) {
+  (void)gt;
+  if (ga.fmt == MGS_FMT_MXFP8) return {gemm_mxfp8_256_kernel, BM2, BN2};
+  if (ga.fmt == MGS_FMT_NVFP4) return {gemm_nvfp4_256_kernel, BM2, BN2};
+  return {gemm_mxfp4_rows_kernel<4, 2>, 64, 32};
+}
+
+}  // namespace
+
 int64_t gemm_tile_count(const GemmArgs& ga, const GroupTable& gt) {
-  if (gt.dev) return capacity_grid(ga, gt, BM2, BN2);
-  return make_table(ga, gt, BM2, BN2).total_tiles;
+  const GemmVariant v = gemm_variant(ga, gt);
+  if (gt.dev) return capacity_grid(ga, gt, v.tm, v.tn);
+  int64_t rows = 0;
+  if (ga.mode == MGS_GEMM_WGRAD) {
+    rows = (ga.m + v.tm - 1) / v.tm * gt.num_groups;
+  } else {
+    for (int g = 0; g < gt.num_groups; ++g) rows += (gt.row_off[g + 1] - gt.row_off[g] + v.tm - 1) / v.tm;
+  }
+  return rows * ((ga.n + v.tn - 1) / v.tn);
 }
 
 hipError_t launch_gemm(const GemmArgs& ga, const GroupTable& gt, hipStream_t st, GemmTable* dev_gemm_table) {
+  const GemmVariant v = gemm_variant(ga, gt);
+  GemmTable tt{};
   if (gt.dev) {
     // device-resident split sizes: the launch's table is built on the device first
-    hipLaunchKernelGGL(gemm_table_kernel, dim3(1), dim3(256), 0, st, gt.dev, ga.mode, ga.m, ga.n, BM2, BN2,
+    hipLaunchKernelGGL(gemm_table_kernel, dim3(1), dim3(256), 0, st, gt.dev, ga.mode, ga.m, ga.n, v.tm, v.tn,
                        gt.total_rows, dev_gemm_table);
-    GemmTable tt{};
     tt.dev = dev_gemm_table;
-    const int64_t grid = capacity_grid(ga, gt, BM2, BN2);
-    if (ga.fmt == MGS_FMT_MXFP8)
-      hipLaunchKernelGGL(gemm_mxfp8_256_kernel, dim3((unsigned)grid), dim3(256), 0, st, ga, tt);
-    else
-      hipLaunchKernelGGL(gemm_nvfp4_256_kernel, dim3((unsigned)grid), dim3(256), 0, st, ga, tt);
-    return hipGetLastError();
-  }
-  if (ga.fmt == MGS_FMT_MXFP8) {
-    const GemmTable tt = make_table(ga, gt, BM2, BN2);
-    if (tt.total_tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL(gemm_mxfp8_256_kernel, dim3((unsigned)tt.grid), dim3(256), 0, st, ga, tt);
+    tt.grid = (int32_t)capacity_grid(ga, gt, v.tm, v.tn);
   } else {
-    const GemmTable tt = make_table(ga, gt, BM2, BN2);
+    tt = make_table(ga, gt, v.tm, v.tn);
     if (tt.total_tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL(gemm_nvfp4_256_kernel, dim3((unsigned)tt.grid), dim3(256), 0, st, ga, tt);
   }
+  hipLaunchKernelGGL(v.kernel, dim3((unsigned)tt.grid), dim3(256), 0, st, ga, tt);
   return hipGetLastError();
 }
 

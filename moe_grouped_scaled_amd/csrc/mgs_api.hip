@@ -4,6 +4,7 @@
 // ops receive split_sizes and derive each group's rows from it): row offsets, padded columnwise
 // token offsets and the per-launch tile lists are computed here on the host and passed to the
 // kernels by value, so no device memory is allocated and nothing is synchronized.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -36,7 +37,7 @@ int ok() {
   return MGS_OK;
 }
 
-bool valid_fmt(int32_t fmt) { return fmt == MGS_FMT_MXFP8 || fmt == MGS_FMT_NVFP4; }
+bool valid_fmt(int32_t fmt) { return fmt == MGS_FMT_MXFP8 || fmt == MGS_FMT_NVFP4 || fmt == MGS_FMT_MXFP4; }
 
 bool is_gated(int kind) { return kind == MGS_ACT_SWIGLU || kind == MGS_ACT_CLAMPED_SWIGLU || kind == MGS_ACT_GLU; }
 
@@ -171,6 +172,16 @@ mgs::GemmTable* dev_gemm_table(const mgs_groups* groups) {
 }
 
 
+// MXFP4 GEMM kernels address the scale arrays through 32-bit offsets: the rowwise scales of A (all rows)
+// and of the weights (all experts) stay below 2^31 bytes.
+int check_gemm_scales(int mode, int fmt, const mgs::GroupTable& gt, int64_t n, int64_t k) {
+  if (fmt != MGS_FMT_MXFP4 || mode == MGS_GEMM_WGRAD) return MGS_OK;
+  const int64_t rows = std::max<int64_t>(gt.total_rows, n * gt.num_groups);
+  if (4 * rows * ((k + 127) / 128) >= (int64_t)1 << 31)
+    return fail(MGS_ERR_SHAPE, "%lld rows x k %lld: a scale array reaches 2 GiB", (long long)rows, (long long)k);
+  return MGS_OK;
+}
+
 int hip_status(hipError_t e) {
   if (e != hipSuccess) return fail(MGS_ERR_HIP, "HIP launch error: %s", hipGetErrorString(e));
   return ok();
@@ -297,9 +308,9 @@ int64_t mgs_qtensor_nbytes(int32_t fmt, int32_t colwise, const mgs_groups* group
     case MGS_NBYTES_SCALES:
       ok();
       if (fmt == MGS_FMT_NVFP4) return r * width / 16;
-      // MXFP8 scales are grouped per 128-wide K step: 4 bytes per row and step
+      // MXFP8 and MXFP4 scales are grouped per 128-wide K step: 4 bytes per row and step
       return colwise ? r * width / 32 : 4 * r * ((width + 127) / 128);
-    case MGS_NBYTES_GROUP_SCALE: ok(); return fmt == MGS_FMT_MXFP8 ? 0 : 4 * (int64_t)gt.num_groups;
+    case MGS_NBYTES_GROUP_SCALE: ok(); return fmt == MGS_FMT_NVFP4 ? 4 * (int64_t)gt.num_groups : 0;
     default: return fail(MGS_ERR_INVALID_ARG, "unknown buffer selector %d", which);
   }
 }
@@ -472,6 +483,7 @@ int mgs_grouped_gemm_mx(int32_t mode, int32_t fmt, const mgs_groups* groups, int
     if ((rc = check_width(k, "k"))) return rc;
     if (m != rows) return fail(MGS_ERR_SHAPE, "m = %lld must equal the split sum %lld", (long long)m, (long long)rows);
   }
+  if ((rc = check_gemm_scales(mode, fmt, gt, n, k))) return rc;
   mgs::GemmArgs ga{};
   ga.mode = mode;
   ga.fmt = fmt;

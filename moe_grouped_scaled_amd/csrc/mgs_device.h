@@ -189,6 +189,33 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   return w;
 }
 
+// ------------------------------------------------------------------------------------------ MXFP4
+
+// E8M0 scale code of a block with maximum magnitude `amax` (>= 0, finite):
+// clamp(floor(log2 amax) - 2 + 127, 0, 254), 0 for amax == 0 or subnormal (see mx_scale_code).
+__device__ __forceinline__ uint32_t mx4_scale_code(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23);
+  return (uint32_t)(e > 2 ? e - 2 : 0);
+}
+
+// MXFP4 encode of the eight values a lane holds of one 32-element block whose maximum magnitude is
+// `amax`: the E8M0 scale code and the eight E2M1 codes in a dword (value 2i in the low nibble of byte
+// i).  The scaled convert divides by the power of two exactly, rounds to nearest-even and saturates
+// at +-6 (checked on the device for every scale code 0..254, the subnormal 2^-127 included).
+struct Mx4 {
+  uint32_t code, q;
+};
+__device__ __forceinline__ Mx4 mx4_encode8(const float (&v)[8], float amax) {
+  Mx4 r;
+  r.code = mx4_scale_code(amax);
+  const float s = mx_scale_value(r.code);
+  r.q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], s, 0);
+  r.q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r.q, v[2], v[3], s, 1);
+  r.q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r.q, v[4], v[5], s, 2);
+  r.q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r.q, v[6], v[7], s, 3);
+  return r;
+}
+
 // per-group encode scale from the group amax: 2688 / amax (1 for amax == 0, FLT_MAX on overflow)
 __device__ __forceinline__ float nv_encode_scale(float amax) {
   if (amax == 0.0f) return 1.0f;

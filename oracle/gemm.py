@@ -13,7 +13,8 @@ Every mode is written as C_g = A_g . B_g^T with both operands stored K-contiguou
   fprop : A = activation rowwise [m_g x K],      B = W_g rowwise [N x K]        -> C [m_g x N]
   dgrad : A = dY rowwise [m_g x N],              B = W_g columnwise [K x N]     -> C [m_g x K]
   wgrad : A = dY columnwise [N_y x mp_g],        B = X columnwise [N_x x mp_g]  -> dW_g [N_y x N_x]
-Operands are dequantized exactly to float64 (MXFP8: e4m3 * 2^(c-127); NVFP4: e2m1 * s_b * S_dec),
+Operands are dequantized exactly to float64 (MXFP8: e4m3 * 2^(c-127); MXFP4: e2m1 * 2^(c-127);
+NVFP4: e2m1 * s_b * S_dec),
 the product is taken in float64, the per-group bias is added, and an empty group's wgrad is zero.
 
 Parity: the all-unit-scale, small-integer-code case reduces exactly to an int64 matmul (pinned in
@@ -23,13 +24,13 @@ the CPU tests); the general case is the definition above.
 import numpy as np
 
 from .codecs import e2m1_decode, e4m3_decode, e8m0_decode, unpack_e2m1
-from .quant import MXFP8, NVFP4, col_offsets, group_offsets, mx_scales_from_kstep
+from .quant import MXFP4, MXFP8, NVFP4, col_offsets, group_offsets, mx_scales_from_kstep
 
 
 def dequant_rows(fmt, data, scales, rows, width, group_scale=None):
     """Dequantize a [rows x width] K-contiguous block-quantized matrix to float64.
 
-    MXFP8 scales are in the K-step grouped layout of that matrix; ``group_scale`` (NVFP4 only) is a
+    MXFP8 and MXFP4 scales are in the K-step grouped layout of that matrix; ``group_scale`` (NVFP4 only) is a
     scalar S_dec applied to the whole matrix.
     """
     if rows == 0:
@@ -40,6 +41,8 @@ def dequant_rows(fmt, data, scales, rows, width, group_scale=None):
         return q * np.repeat(s, 32, axis=1)
     codes = unpack_e2m1(np.asarray(data, np.uint8).reshape(rows, width // 2))
     q = e2m1_decode(codes)
+    if fmt == MXFP4:
+        return q * np.repeat(e8m0_decode(mx_scales_from_kstep(scales, rows, width)), 32, axis=1)
     s = e4m3_decode(np.asarray(scales, np.uint8).reshape(rows, width // 16))
     return q * np.repeat(s, 16, axis=1) * float(group_scale)
 
@@ -47,10 +50,10 @@ def dequant_rows(fmt, data, scales, rows, width, group_scale=None):
 def dequant_row_grouped(fmt, data, scales, split_sizes, width, group_scale=None):
     """Dequantize a rowwise grouped qtensor [M x width]; NVFP4 applies each group's S_dec.
 
-    MXFP8 scales are K-step grouped over the whole [M x width] matrix."""
+    MXFP8 and MXFP4 scales are K-step grouped over the whole [M x width] matrix."""
     off = group_offsets(split_sizes)
     m = int(off[-1])
-    if fmt == MXFP8:
+    if fmt in (MXFP8, MXFP4):
         return dequant_rows(fmt, data, scales, m, width)
     out = np.zeros((m, width))
     bpr_d, bpr_s = width // 2, width // 16
@@ -66,7 +69,7 @@ def dequant_col_grouped(fmt, data, scales, split_sizes, width, group_scale=None)
     coff = col_offsets(split_sizes)
     mats = []
     db = 1 if fmt == MXFP8 else 2
-    sb = 32 if fmt == MXFP8 else 16
+    sb = 16 if fmt == NVFP4 else 32
     for g in range(len(split_sizes)):
         mp = int(coff[g + 1] - coff[g])
         d0 = int(width * coff[g] // db)

@@ -39,7 +39,7 @@ from .gemm import (
     gemm_grouped_k,
     gemm_grouped_m,
 )
-from .quant import MXFP8, NVFP4, col_offsets, group_offsets, quantize_grouped
+from .quant import MXFP8, NVFP4, col_offsets, group_offsets, qtensor_nbytes, quantize_grouped
 
 
 def _bf16(x64):
@@ -127,7 +127,4 @@ def recompute_memory_drop(fmt, splits, width_out):
     activation output (data + scales), i.e. what the forward no longer writes.  [P1] Description,
     first list, last bullet: memory must drop, measured between forward and backward.
     """
-    rows = int(col_offsets(splits)[-1])
-    if fmt == MXFP8:
-        return rows * width_out + rows * width_out // 32
-    return rows * width_out // 2 + rows * width_out // 16
+    return sum(qtensor_nbytes(fmt, True, splits, width_out))

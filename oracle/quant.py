@@ -1,4 +1,5 @@
-"""Grouped block quantization: MXFP8 (E4M3 + E8M0 per 32) and NVFP4 (E2M1 + E4M3 per 16 + FP32 per tensor).
+"""Grouped block quantization: MXFP8 (E4M3 + E8M0 per 32), NVFP4 (E2M1 + E4M3 per 16 + FP32 per tensor) and
+MXFP4 (E2M1 + E8M0 per 32).
 
 Test infrastructure only (see the package header).
 
@@ -11,6 +12,8 @@ Sources:
     columnwise copy feeds the weight-gradient GEMM.
   * OCP Microscaling Formats v1.0: MXFP8 E4M3 block of 32 with shared scale
     X = 2^(floor(log2(amax)) - emax_elem), emax_elem = 8 for E4M3 (448 = 1.75 * 2^8).
+  * OCP Microscaling Formats v1.0, MXFP4: E2M1 elements in blocks of 32 with the same shared scale rule,
+    emax_elem = 2 (6 = 1.5 * 2^2); elements round to nearest-even and saturate at 6.
   * The NVFP4 recipe: a per-tensor FP32 encode scale S_enc = (448 * 6) / amax_tensor, a per-16-block
     E4M3 decode scale s_b = E4M3(amax_b / 6 * S_enc), elements E2M1(y * S_enc / s_b); the stored
     per-tensor value is S_dec = 1 / S_enc, and y ~= e2m1 * s_b * S_dec.
@@ -34,6 +37,7 @@ Buffer layouts produced here are the library's documented qtensor layouts:
   colwise MXFP8 : per group g at data offset W*coff[g]:    data [W, mp_g],
                   scales at W*coff[g]/32:                  K-step grouped over [W, mp_g]
   colwise NVFP4 : per group g at data offset W*coff[g]/2: data [W, mp_g/2],     scales [W, mp_g/16]
+  MXFP4         : data as NVFP4's (two codes per byte), scales as MXFP8's (K-step grouped)
   with mp_g = roundup(m_g, 128) and coff[g] = sum_{h<g} mp_h.
   "K-step grouped" (MXFP8 scales of an [R x K] matrix): the four 32-block scales of each 128-wide K
   step are stored together per row, steps outermost -- the byte of (row r, block kb) is at
@@ -68,7 +72,8 @@ from .codecs import (
 
 MXFP8 = "mxfp8"
 NVFP4 = "nvfp4"
-BLOCK = {MXFP8: 32, NVFP4: 16}
+MXFP4 = "mxfp4"
+BLOCK = {MXFP8: 32, NVFP4: 16, MXFP4: 32}
 COL_ALIGN = 128
 FLT_MAX = float(np.finfo(np.float32).max)
 
@@ -132,6 +137,22 @@ def mx_scales_from_kstep(flat, r, k):
     for kb in range(nkb):
         out[:, kb] = a[kb // 4, :, kb % 4]
     return out
+
+
+# ----------------------------------------------------------------------------- MXFP4
+
+def mxfp4_quantize_rows(y32):
+    """Quantize float32 values (given as float64) along the last axis in blocks of 32: packed E2M1 codes
+    [rows, w/2] and E8M0 codes [rows, w/32], code = clamp(floor(log2 amax) - 2 + 127, 0, 254), 0 for a
+    zero block."""
+    y = np.asarray(y32, dtype=np.float64)
+    rows, w = y.shape
+    assert w % 32 == 0
+    blocks = y.reshape(rows, w // 32, 32)
+    amax = np.max(np.abs(blocks), axis=-1)
+    code = np.where(amax > 0, np.clip(floor_log2(np.where(amax > 0, amax, 1.0)) - 2 + 127, 0, 254), 0).astype(np.uint8)
+    q = e2m1_encode(blocks / np.ldexp(1.0, code.astype(np.int64) - 127)[..., None])
+    return pack_e2m1(q.reshape(rows, w)), code
 
 
 # ----------------------------------------------------------------------------- NVFP4
@@ -227,6 +248,8 @@ def quantize_grouped(y32, split_sizes, fmt, rowwise=True, colwise=True, group_am
     if rowwise:
         if fmt == MXFP8:
             d, s = mxfp8_quantize_rows(y) if m_total else (np.zeros((0, w), np.uint8), np.zeros((0, w // 32), np.uint8))
+        elif fmt == MXFP4:
+            d, s = mxfp4_quantize_rows(y) if m_total else (np.zeros((0, w // 2), np.uint8), np.zeros((0, w // 32), np.uint8))
         else:
             parts_d, parts_s = [], []
             for g in range(e):
@@ -239,7 +262,7 @@ def quantize_grouped(y32, split_sizes, fmt, rowwise=True, colwise=True, group_am
             d = np.concatenate(parts_d) if parts_d else np.zeros((0, w // 2), np.uint8)
             s = np.concatenate(parts_s) if parts_s else np.zeros((0, w // 16), np.uint8)
         out["row_data"] = d.reshape(-1)
-        out["row_scales"] = mx_scales_to_kstep(s) if fmt == MXFP8 else s.reshape(-1)
+        out["row_scales"] = s.reshape(-1) if fmt == NVFP4 else mx_scales_to_kstep(s)
     if colwise:
         assert rht is None or fmt == NVFP4, "the Hadamard transform applies to NVFP4 columnwise copies"
         col_t, col_enc = [], s_enc
@@ -261,8 +284,8 @@ def quantize_grouped(y32, split_sizes, fmt, rowwise=True, colwise=True, group_am
             if mp == 0:
                 continue
             yt = col_t[g]
-            if fmt == MXFP8:
-                d_g, s_g = mxfp8_quantize_rows(yt)
+            if fmt in (MXFP8, MXFP4):
+                d_g, s_g = mxfp8_quantize_rows(yt) if fmt == MXFP8 else mxfp4_quantize_rows(yt)
                 s_g = mx_scales_to_kstep(s_g)
             else:
                 d_g, s_g = nvfp4_quantize_rows(yt, col_enc[g])
@@ -276,8 +299,9 @@ def quantize_grouped(y32, split_sizes, fmt, rowwise=True, colwise=True, group_am
 def qtensor_nbytes(fmt, colwise, split_sizes, width):
     """(data bytes, scale bytes) of a grouped qtensor in the documented layout."""
     rows = int(col_offsets(split_sizes)[-1]) if colwise else int(np.sum(split_sizes))
-    if fmt == MXFP8:
+    if fmt in (MXFP8, MXFP4):
+        data = rows * width if fmt == MXFP8 else rows * width // 2
         if colwise:   # per group [width x mp_g], mp_g a multiple of 128
-            return rows * width, rows * width // 32
-        return rows * width, 4 * rows * ((width + 127) // 128)
+            return data, rows * width // 32
+        return data, 4 * rows * ((width + 127) // 128)
     return rows * width // 2, rows * width // 16
