@@ -65,6 +65,7 @@ extern "C" {
 
 #define MGS_ABI_VERSION 8
 #define MGS_MAX_GROUPS 256
+#define MGS_MAX_TOPK 16
 /* Size of the static per-device scratch of mgs_grouped_scaled_act_bwd_noalloc (16 MiB). */
 #define MGS_NOALLOC_SCRATCH_BYTES ((int64_t)16 << 20)
 
@@ -339,6 +340,84 @@ int mgs_grouped_gemm_mx_fprop_act(const mgs_groups* groups, int64_t m, int64_t n
  *   x_bf16 [M x width] BF16; out [E x width] FP32 (empty groups give zeros). */
 int mgs_grouped_col_sum(const mgs_groups* groups, int64_t width, const void* x_bf16, float* out,
                         void* stream);
+
+/* ---- Routing around the expert MLP ---------------------------------------------------------------
+ * [P2] sequence diagram: the grouped calls above take rows sorted by expert with split_sizes.  These
+ * calls make both from a router's logits, and bring the expert outputs back into token order; nothing
+ * leaves the device, so a captured graph follows each replay's routing (mgs_groups_update takes
+ * split_sizes as it is written here).  A slot is one (token, choice) pair, numbered token * topk + choice.
+ * Experts 1 .. MGS_MAX_GROUPS, topk 1 .. MGS_MAX_TOPK, tokens * topk below 2^31; tokens == 0 is allowed.
+ * Every pointer is a DEVICE pointer but the params.  Results are deterministic. */
+
+typedef enum { MGS_SCORE_SOFTMAX = 0, MGS_SCORE_SIGMOID = 1 } mgs_score;
+
+typedef struct {
+  int32_t score;       /* mgs_score */
+  int32_t renormalize; /* nonzero: the picked scores are divided by their sum */
+  float scale;         /* finite factor on the weights */
+} mgs_route_params;
+
+/* Router: the topk largest logits of every token, in descending order (equal logits: the lower expert
+ * first; NaN ranks above everything), and their weights
+ *   p = softmax(logits) over all experts, or 1 / (1 + exp(-logit)) each,
+ *   w = scale * p, or with renormalize scale * p / (sum of the token's picked p).
+ * An expert whose logit is -inf is not available: it is never picked, and a choice that finds no
+ * available expert gets expert -1 and weight 0 (a token whose logits are all -inf gets none at all).
+ * NaN or +inf logits give NaN weights as the formulas say; sigmoid scores that all underflow to 0 keep
+ * weights of 0 when renormalized.
+ *   logits      [tokens x experts] BF16 or F32 (logits_dtype), row stride ld >= experts elements
+ *   expert_idx  [tokens x topk] int32; weights [tokens x topk] FP32 */
+int mgs_moe_route(const mgs_route_params* params, int64_t tokens, int32_t experts, int32_t topk,
+                  const void* logits, int32_t logits_dtype, int64_t ld, int32_t* expert_idx, float* weights,
+                  void* stream);
+
+/* The logits' gradient of the router's weights: dlogits [tokens x experts], of the logits' type, row
+ * stride ld_dlogits, every element written (zeros where the formulas give none).  expert_idx is the
+ * forward's; dweights [tokens x topk] FP32 (ignored where expert_idx is -1). */
+int mgs_moe_route_bwd(const mgs_route_params* params, int64_t tokens, int32_t experts, int32_t topk,
+                      const void* logits, int32_t logits_dtype, int64_t ld, const int32_t* expert_idx,
+                      const float* dweights, void* dlogits, int64_t ld_dlogits, void* stream);
+
+/* Workspace bytes of mgs_moe_dispatch.  Negative MGS_ERR_* on invalid arguments. */
+int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts);
+
+/* Tokens into expert order: a stable sort of the slots by expert, and the token rows copied to it.
+ *   expert_idx   [tokens x topk] int32; an entry outside [0, experts) is a slot without an expert
+ *   row_of_slot  [tokens x topk] int32, required: the slot's row in expert order, -1 without an expert
+ *   split_sizes  [experts] int64, required: rows of each expert
+ *   x            [tokens x hidden] BF16 or F32 (dtype), row stride ldx; NULL (with rows NULL): only the sort
+ *   rows         [num_rows x hidden] contiguous, num_rows >= tokens * topk: rows[row_of_slot[s]] = x[token];
+ *                rows past the last used one are left as they were
+ *   weights, row_weights  both or neither: row_weights[row_of_slot[s]] = weights[s] ([tokens x topk], the
+ *                per-row scale `probs` of the activation calls)
+ *   workspace    mgs_moe_dispatch_workspace_bytes() bytes of scratch, caller-owned, contents undefined
+ *                before and after; calls sharing it must not overlap */
+int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_t* expert_idx, int64_t hidden,
+                     int32_t dtype, const void* x, int64_t ldx, const float* weights, void* rows,
+                     int64_t num_rows, float* row_weights, int32_t* row_of_slot, int64_t* split_sizes,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradient of the dispatch: dx[token] = the sum of its slots' drows (in slot order, FP32, one rounding),
+ * and with drow_weights [num_rows] and dweights [tokens x topk] (both or neither) dweights[s] =
+ * drow_weights[row_of_slot[s]] (the activation backward's dprobs), 0 for a slot without a row.
+ * Rows outside [0, num_rows) in row_of_slot count as no row, here and below. */
+int mgs_moe_dispatch_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype,
+                         const int32_t* row_of_slot, int64_t num_rows, const void* drows,
+                         const float* drow_weights, void* dx, int64_t lddx, float* dweights, void* stream);
+
+/* Expert outputs back into token order: y[token] = sum over its slots of w * rows[row_of_slot[s]], in slot
+ * order in FP32, one rounding; weights [tokens x topk] NULL means 1 (where the experts applied them).  A
+ * token without any row gets zeros.  rows [num_rows x hidden] contiguous, y row stride ldy. */
+int mgs_moe_combine(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, const int32_t* row_of_slot,
+                    int64_t num_rows, const void* rows, const float* weights, void* y, int64_t ldy,
+                    void* stream);
+
+/* Gradient of the combine: drows[row_of_slot[s]] = w * dy[token] (nullable; rows that no slot has are
+ * left as they were) and dweights[s] = <dy[token], rows[row_of_slot[s]]> (nullable; needs rows; 0 for a slot
+ * without a row).  At least one of them is requested. */
+int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype,
+                        const int32_t* row_of_slot, int64_t num_rows, const void* dy, int64_t lddy,
+                        const void* rows, const float* weights, void* drows, float* dweights, void* stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,8 @@ GEMM_MODE = {"fprop": 0, "dgrad": 1, "wgrad": 2}
 DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 NBYTES = {"data": 0, "scales": 1, "group_scale": 2}
 MAX_GROUPS = 256
+MAX_TOPK = 16
+SCORE = {"softmax": 0, "sigmoid": 1}
 
 
 class MgsError(RuntimeError):
@@ -46,6 +48,10 @@ class Groups(ctypes.Structure):
 class QBuf(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("group_scale", ctypes.c_void_p), ("rht", ctypes.c_uint32)]
+
+
+class RouteParams(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 RHT_ON = 1 << 16  # mgs_qbuf.rht: bit 16 enables the Hadamard transform, bits 0..15 are its signs
@@ -78,6 +84,15 @@ def _load():
         "mgs_grouped_gemm_mx_fprop_act": (ctypes.c_int, [pgr, i64, i64, i64, pq, pq, vp, vp, pact, vp, i32,
                                                          pq, vp]),
         "mgs_grouped_col_sum": (ctypes.c_int, [pgr, i64, vp, vp, vp]),
+        "mgs_moe_route": (ctypes.c_int, [ctypes.POINTER(RouteParams), i64, i32, i32, vp, i32, i64, vp, vp, vp]),
+        "mgs_moe_route_bwd": (ctypes.c_int, [ctypes.POINTER(RouteParams), i64, i32, i32, vp, i32, i64, vp, vp, vp,
+                                             i64, vp]),
+        "mgs_moe_dispatch_workspace_bytes": (i64, [i64, i32, i32]),
+        "mgs_moe_dispatch": (ctypes.c_int, [i64, i32, i32, vp, i64, i32, vp, i64, vp, vp, i64, vp, vp, vp, vp, i64,
+                                            vp]),
+        "mgs_moe_dispatch_bwd": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp]),
+        "mgs_moe_combine": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, vp, vp, i64, vp]),
+        "mgs_moe_combine_bwd": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -92,7 +107,8 @@ EXPORTED = ("mgs_abi_version", "mgs_last_error", "mgs_groups_table_bytes", "mgs_
             "mgs_grouped_scaled_act_fwd_f32",
             "mgs_grouped_scaled_act_bwd", "mgs_grouped_scaled_act_bwd_noalloc", "mgs_act_bwd_workspace_bytes", "mgs_grouped_mx_quantize",
             "mgs_grouped_mx_quantize_workspace_bytes", "mgs_grouped_gemm_mx", "mgs_grouped_gemm_mx_fprop_act",
-            "mgs_grouped_col_sum")
+            "mgs_grouped_col_sum", "mgs_moe_route", "mgs_moe_route_bwd", "mgs_moe_dispatch_workspace_bytes",
+            "mgs_moe_dispatch", "mgs_moe_dispatch_bwd", "mgs_moe_combine", "mgs_moe_combine_bwd")
 
 
 def _check(rc):

@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmgs.so")
-SOURCES = ["mgs_api.hip", "act_quant.hip", "gemm_mx.hip"]
+SOURCES = ["mgs_api.hip", "act_quant.hip", "gemm_mx.hip", "moe_route.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950",

@@ -21,8 +21,10 @@
 static __device__ __align__(256) uint8_t scratch[MGS_NOALLOC_SCRATCH_BYTES];
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace mgs {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -36,6 +38,13 @@ int ok() {
   g_err[0] = '\0';
   return MGS_OK;
 }
+
+}  // namespace mgs
+
+namespace {
+
+using mgs::fail;
+using mgs::ok;
 
 bool valid_fmt(int32_t fmt) { return fmt == MGS_FMT_MXFP8 || fmt == MGS_FMT_NVFP4 || fmt == MGS_FMT_MXFP4; }
 

@@ -9,6 +9,10 @@
 
 namespace mgs {
 
+// The error state of the C ABI (thread-local message): fail() records one and returns `code`, ok() clears it.
+int fail(int code, const char* fmt, ...);
+int ok();
+
 // Rows of one panel: a panel is 32 consecutive rows of one group, the unit of the columnwise
 // quantization blocks (32 for MXFP8, 2 x 16 for NVFP4).
 constexpr int PANEL_ROWS = 32;

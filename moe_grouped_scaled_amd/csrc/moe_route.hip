@@ -1,0 +1,700 @@
+// Routing around the expert MLP for gfx950: the top-k experts of every token with their weights, tokens
+// sorted by expert and copied into expert order, expert outputs summed back per token, and the gradients
+// of all of them.  Entry points, host validation and kernels.
+//
+// The expert MLP takes rows sorted by expert and their split sizes (page "Activation + GroupedLinear
+// Fusion for MOE", sequence diagram); these calls make both from a router's logits and undo the order
+// afterwards, with the split sizes left in device memory, so a captured graph follows the routing.
+//
+// A slot is one (token, choice) pair, numbered token * topk + choice.
+#include <algorithm>
+#include <initializer_list>
+#include <type_traits>
+
+#include "mgs_device.h"
+
+namespace mgs {
+namespace {
+
+// ------------------------------------------------------------------------------------------ router
+//
+// Sixteen lanes (one DPP row) own a token, four tokens a wave; lane l holds the logits of experts
+// l, l + 16, ... as integer keys that order like the values.  A pick is a maximum over the lane's keys and
+// four DPP steps, then the lowest expert that holds it the same way.
+
+constexpr int ROUTE_LANES = 16;
+constexpr int DPP_ROW_ROR1 = 0x121, DPP_ROW_ROR2 = 0x122;
+
+__device__ __forceinline__ uint32_t row_umax(uint32_t v) {
+  v = umax(v, dpp_u<DPP_ROW_ROR8>(v));
+  v = umax(v, dpp_u<DPP_ROW_ROR4>(v));
+  v = umax(v, dpp_u<DPP_ROW_ROR2>(v));
+  return umax(v, dpp_u<DPP_ROW_ROR1>(v));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<DPP_ROW_ROR8>(v);
+  v += dpp_f<DPP_ROW_ROR4>(v);
+  v += dpp_f<DPP_ROW_ROR2>(v);
+  return v + dpp_f<DPP_ROW_ROR1>(v);
+}
+
+// Integer that orders like the logit: -0 equals +0 (the addition), NaN above everything.
+__device__ __forceinline__ uint32_t logit_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return k == 0xffffffffu ? __uint_as_float(0x7fc00000u) : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+constexpr uint32_t KEY_NEG_INF = 0x007fffffu;  // key of -inf; experts that cannot be picked are at or below it
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const T* p);
+template <>
+__device__ __forceinline__ float load_logit<float>(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float load_logit<uint16_t>(const uint16_t* p) { return bf16lo(*p); }
+__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, 0.0f); }
+
+struct RouteArgs {
+  int64_t tokens;
+  int experts, topk, score, renormalize;
+  float scale;
+  int64_t ld, ldd;
+};
+
+template <typename T, int EPL>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __restrict__ logits,
+                                                    int32_t* __restrict__ idx, float* __restrict__ weights) {
+  const int l = threadIdx.x & (ROUTE_LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / ROUTE_LANES) + (threadIdx.x >> 4);
+  const bool there = t < a.tokens;
+  uint32_t key[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = ROUTE_LANES * j + l;
+    key[j] = there && e < a.experts ? logit_key(load_logit(logits + t * a.ld + e)) : 0u;
+  }
+  const bool full_sum = a.score == MGS_SCORE_SOFTMAX && !a.renormalize;
+  float top = 0.0f, sum = 0.0f, mine = 0.0f;  // lane c keeps choice c's score
+  int pick = -1;
+  for (int c = 0; c < a.topk; ++c) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) m = umax(m, key[j]);
+    m = row_umax(m);
+    int at = -1;
+#pragma unroll
+    for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? ROUTE_LANES * j + l : at;
+    // lowest expert among the lanes that hold m, as a maximum of the complement
+    const int e = (int)~row_umax(at < 0 ? 0u : ~(uint32_t)at);
+    const bool ok = m > KEY_NEG_INF;
+    const float x = key_logit(m);
+    if (c == 0) {
+      top = ok ? x : 0.0f;
+      if (full_sum) {
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) s += key[j] > KEY_NEG_INF ? expf(key_logit(key[j]) - top) : 0.0f;
+        sum = row_sum(s);
+      }
+    }
+    float p = 0.0f;
+    if (ok) p = a.score == MGS_SCORE_SOFTMAX ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+    if (!full_sum && a.renormalize) sum += p;
+    if (l == c) {
+      mine = p;
+      pick = ok ? e : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = ROUTE_LANES * j + l == e ? 0u : key[j];
+  }
+  if (there && l < a.topk) {
+    idx[t * a.topk + l] = pick;
+    float w = mine;
+    // a sum of 0 (sigmoid scores that all underflow) leaves the weights 0
+    if (pick >= 0 && (full_sum || a.renormalize) && sum != 0.0f) w = mine / sum;
+    weights[t * a.topk + l] = w * a.scale;
+  }
+}
+
+// Gradient of the weights with respect to the logits.  Lane c of a token's sixteen holds choice c.  The
+// differences g_j - sum_i w_i g_i of the softmax and of the renormalization cancel where one weight is
+// near 1, so they are taken as sum_i w_i (g_j - g_i), plus g_j times the weight of the experts not picked.
+template <typename T, int EPL>
+__global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __restrict__ logits,
+                                                        const int32_t* __restrict__ idx,
+                                                        const float* __restrict__ dweights,
+                                                        T* __restrict__ dlogits) {
+  const int l = threadIdx.x & (ROUTE_LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / ROUTE_LANES) + (threadIdx.x >> 4);
+  const bool there = t < a.tokens;
+  int e = -1;
+  float g = 0.0f, x = 0.0f;
+  if (there && l < a.topk) {
+    e = idx[t * a.topk + l];
+    if (e < 0 || e >= a.experts) e = -1;
+    if (e >= 0) {
+      g = dweights[t * a.topk + l] * a.scale;
+      x = load_logit(logits + t * a.ld + e);
+    }
+  }
+  const bool softmax = a.score == MGS_SCORE_SOFTMAX, dense = softmax && !a.renormalize;
+  float p = 0.0f, q = 0.0f;  // the choice's score; 1 - score of a sigmoid
+  float ex[EPL];
+  float rest = 0.0f;         // softmax weight of the experts that were not picked
+  if (softmax) {
+    // maximum and sum over the picked experts, or over all of them
+    float top = row_umax(e >= 0 ? logit_key(x) : 0u) > KEY_NEG_INF ? key_logit(row_umax(e >= 0 ? logit_key(x) : 0u)) : 0.0f;
+    float sum;
+    p = e >= 0 ? expf(x - top) : 0.0f;
+    if (dense) {
+      float s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const int at = ROUTE_LANES * j + l;
+        float v = there && at < a.experts ? load_logit(logits + t * a.ld + at) : 0.0f;
+        ex[j] = there && at < a.experts ? expf(v - top) : 0.0f;
+        bool picked = false;
+        for (int i = 0; i < a.topk; ++i) picked |= __shfl(e, i, ROUTE_LANES) == at;
+        s += picked ? 0.0f : ex[j];
+      }
+      rest = row_sum(s);
+      sum = rest + row_sum(p);
+      const float div = sum != 0.0f ? sum : 1.0f;  // 0: no expert is available
+      rest /= div;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) ex[j] /= div;
+    } else {
+      sum = row_sum(p);
+    }
+    p = e >= 0 ? p / sum : 0.0f;
+  } else if (e >= 0) {
+    const float z = expf(-fabsf(x));  // in (0, 1]: neither form below overflows
+    p = (x >= 0.0f ? 1.0f : z) / (1.0f + z);
+    q = (x >= 0.0f ? z : 1.0f) / (1.0f + z);
+  }
+  float w = p;
+  if (!softmax && a.renormalize) {
+    const float s = row_sum(p);
+    w = e >= 0 && s != 0.0f ? p / s : 0.0f;
+  }
+  float d;
+  if (dense || a.renormalize) {
+    float s = 0.0f;
+    for (int i = 0; i < a.topk; ++i) {
+      const float wi = __shfl(w, i, ROUTE_LANES), gi = __shfl(g, i, ROUTE_LANES);
+      s = __builtin_fmaf(wi, g - gi, s);
+    }
+    d = w * __builtin_fmaf(g, rest, s);
+    if (!softmax) d *= q;
+  } else {
+    d = g * p * q;
+  }
+  const float others = dense ? -row_sum(w * g) : 0.0f;  // of the experts not picked: -p_e sum_i w_i g_i
+  float out[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) out[j] = dense ? ex[j] * others : 0.0f;
+  for (int i = 0; i < a.topk; ++i) {
+    const int ei = __shfl(e, i, ROUTE_LANES);
+    const float di = __shfl(d, i, ROUTE_LANES);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) out[j] = ei == ROUTE_LANES * j + l ? di : out[j];
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int at = ROUTE_LANES * j + l;
+    if (there && at < a.experts) store_value(dlogits + t * a.ldd + at, out[j]);
+  }
+}
+
+// ------------------------------------------------------------------------------------------ sorting
+//
+// A stable counting sort of the slots by expert: row_of_slot[s] is the number of slots with a smaller
+// expert plus those with the same expert and a smaller number; slots without an expert get -1.  The
+// result is fixed by the indices alone.
+
+// Slots per histogram block: at most 128 blocks up to 524288 slots, so that a block's sum over the
+// blocks before it stays short.
+__host__ __device__ inline int sort_chunk(int64_t slots) { return slots <= 131072 ? 1024 : 4096; }
+
+__device__ __forceinline__ int slot_expert(const int32_t* __restrict__ idx, int64_t s, int64_t slots, int experts) {
+  const int e = s < slots ? idx[s] : -1;
+  return e >= 0 && e < experts ? e : -1;
+}
+
+__global__ __launch_bounds__(256) void sort_count_kernel(int64_t slots, int experts, int chunk,
+                                                         const int32_t* __restrict__ idx, int32_t* __restrict__ counts) {
+  __shared__ int32_t h[MGS_MAX_GROUPS];
+  h[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t s0 = (int64_t)blockIdx.x * chunk;
+  for (int i = threadIdx.x; i < chunk; i += 256) {
+    const int e = slot_expert(idx, s0 + i, slots, experts);
+    if (e >= 0) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < experts) counts[(int64_t)blockIdx.x * experts + threadIdx.x] = h[threadIdx.x];
+}
+
+// Exclusive sum over the 256 threads of a workgroup.
+__device__ __forceinline__ int block_exclusive(int v, int32_t* lds) {
+  const int t = threadIdx.x;
+  lds[t] = v;
+  __syncthreads();
+  for (int d = 1; d < 256; d <<= 1) {
+    const int o = t >= d ? lds[t - d] : 0;
+    __syncthreads();
+    lds[t] += o;
+    __syncthreads();
+  }
+  return lds[t] - v;
+}
+
+__global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int experts, int chunk,
+                                                        const int32_t* __restrict__ idx,
+                                                        const int32_t* __restrict__ counts,
+                                                        int32_t* __restrict__ row_of_slot,
+                                                        int64_t* __restrict__ splits) {
+  __shared__ int32_t scan[256];
+  __shared__ int32_t next[4][MGS_MAX_GROUPS];  // the next row of each expert, per wave
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int before = 0, total = 0;
+  if (t < experts) {
+    const int nb = gridDim.x;
+    for (int b = 0; b < nb; ++b) {
+      const int v = counts[(int64_t)b * experts + t];
+      before += b < (int)blockIdx.x ? v : 0;
+      total += v;
+    }
+    if (blockIdx.x == 0) splits[t] = total;
+  }
+  const int base = block_exclusive(total, scan) + before;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) next[w][t] = 0;
+  __syncthreads();
+  // wave w owns the w-th quarter of the chunk; its rows follow those of the waves before it
+  const int per = chunk / 4;
+  const int64_t s0 = (int64_t)blockIdx.x * chunk + (int64_t)wave * per;
+  for (int i = lane; i < per; i += 64) {
+    const int e = slot_expert(idx, s0 + i, slots, experts);
+    if (e >= 0) atomicAdd(&next[wave][e], 1);
+  }
+  __syncthreads();
+  int r = base;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int c = next[w][t];
+    next[w][t] = r;
+    r += c;
+  }
+  __syncthreads();
+  for (int i = lane; i < per; i += 64) {
+    const int64_t s = s0 + i;
+    const int e = slot_expert(idx, s, slots, experts);
+    // lanes with the same expert: one ballot per bit of it
+    uint64_t same = __ballot(e >= 0);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const uint64_t v = __ballot((e >> b) & 1);
+      same &= (e >> b) & 1 ? v : ~v;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    int row = -1;
+    if (e >= 0) row = next[wave][e] + rank;
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && rank == 0) next[wave][e] += __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (s < slots) row_of_slot[s] = row;
+  }
+}
+
+// ------------------------------------------------------------------------------------------ row copies
+//
+// Rows are moved in units of V elements (16 bytes where widths, strides and addresses allow it, else
+// single elements).  A token's units are spread over `tpt` threads, a power of two up to 256.
+
+template <typename T, int V>
+__device__ __forceinline__ void unit_load(const T* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    unpack8(*reinterpret_cast<const uint4*>(p), v);
+  } else if constexpr (V == 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    v[0] = load_logit(p);
+  }
+}
+
+// The data registers of a 16-byte store stay live through two wait states after it (a VALU write to one of
+// them in the next instruction changed what part of the wave stored).
+__device__ __forceinline__ void store16(void* p, uint4 d) {
+  typedef unsigned int v4u_t __attribute__((ext_vector_type(4)));
+  const v4u_t v = {d.x, d.y, d.z, d.w};
+  *reinterpret_cast<v4u_t*>(p) = v;
+  asm volatile("s_nop 1" ::"v"(v));
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void unit_store(T* p, const float (&v)[V]) {
+  if constexpr (V == 8) {
+    store16(p, pack8_bf16(v));
+  } else if constexpr (V == 4) {
+    store16(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+  } else {
+    store_value(p, v[0]);
+  }
+}
+
+// the same bits, unconverted
+template <typename T, int V>
+struct Raw { typedef uint4 type; };
+template <>
+struct Raw<float, 1> { typedef float type; };
+template <>
+struct Raw<uint16_t, 1> { typedef uint16_t type; };
+__device__ __forceinline__ void raw_store(uint4* p, uint4 v) { store16(p, v); }
+__device__ __forceinline__ void raw_store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void raw_store(uint16_t* p, uint16_t v) { *p = v; }
+
+struct MoveArgs {
+  int64_t tokens, hidden, ld;  // ld: row stride of the token-side tensor (elements)
+  int topk, experts;
+  int32_t num_rows;            // rows of the expert-side tensor
+  int tpt_log2;                // threads per token
+};
+
+// row of a slot, -1 where it has none
+__device__ __forceinline__ int slot_row(const MoveArgs& a, const int32_t* __restrict__ row_of_slot, int64_t t, int c) {
+  const int r = row_of_slot[t * a.topk + c];
+  return r >= 0 && r < a.num_rows ? r : -1;
+}
+
+// x row of every token into the rows of its slots
+template <typename T, int V>
+__global__ __launch_bounds__(256) void scatter_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
+                                                      const T* __restrict__ x, const float* __restrict__ weights,
+                                                      T* __restrict__ rows, float* __restrict__ row_weights) {
+  typedef typename Raw<T, V>::type R;
+  const int u = threadIdx.x & ((1 << a.tpt_log2) - 1);
+  const int64_t t = ((int64_t)blockIdx.x << (8 - a.tpt_log2)) + (threadIdx.x >> a.tpt_log2);
+  if (t >= a.tokens) return;
+  if (row_weights && u < a.topk) {
+    for (int c = u; c < a.topk; c += 1 << a.tpt_log2) {
+      const int r = slot_row(a, row_of_slot, t, c);
+      if (r >= 0) row_weights[r] = weights[t * a.topk + c];
+    }
+  }
+  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V << a.tpt_log2) {
+    const R v = *reinterpret_cast<const R*>(x + t * a.ld + h);
+    for (int c = 0; c < a.topk; ++c) {
+      const int r = slot_row(a, row_of_slot, t, c);
+      if (r >= 0) raw_store(reinterpret_cast<R*>(rows + (int64_t)r * a.hidden + h), v);
+    }
+  }
+}
+
+// y of every token: the sum over its slots' rows in slot order, in FP32, with weights if given
+template <typename T, int V>
+__global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
+                                                      const T* __restrict__ rows, const float* __restrict__ weights,
+                                                      T* __restrict__ y, const float* __restrict__ drow_weights,
+                                                      float* __restrict__ dweights) {
+  const int u = threadIdx.x & ((1 << a.tpt_log2) - 1);
+  const int64_t t = ((int64_t)blockIdx.x << (8 - a.tpt_log2)) + (threadIdx.x >> a.tpt_log2);
+  if (t >= a.tokens) return;
+  if (dweights) {
+    for (int c = u; c < a.topk; c += 1 << a.tpt_log2) {
+      const int r = slot_row(a, row_of_slot, t, c);
+      dweights[t * a.topk + c] = r >= 0 ? drow_weights[r] : 0.0f;
+    }
+  }
+  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V << a.tpt_log2) {
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int c = 0; c < a.topk; ++c) {
+      const int r = slot_row(a, row_of_slot, t, c);
+      if (r < 0) continue;
+      float v[V];
+      unit_load<T, V>(rows + (int64_t)r * a.hidden + h, v);
+      const float w = weights ? weights[t * a.topk + c] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+    }
+    unit_store<T, V>(y + t * a.ld + h, acc);
+  }
+}
+
+// d(rows) = w dy and d(w) = <dy, rows> of every slot; one workgroup per token
+template <typename T, int V>
+__global__ __launch_bounds__(256) void combine_bwd_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
+                                                          const T* __restrict__ dy, const T* __restrict__ rows,
+                                                          const float* __restrict__ weights, T* __restrict__ drows,
+                                                          float* __restrict__ dweights) {
+  __shared__ float part[4];
+  const int64_t t = blockIdx.x;
+  for (int c = 0; c < a.topk; ++c) {
+    const int r = slot_row(a, row_of_slot, t, c);
+    if (r < 0) {
+      if (dweights && threadIdx.x == 0) dweights[t * a.topk + c] = 0.0f;
+      continue;
+    }
+    const float w = weights ? weights[t * a.topk + c] : 1.0f;
+    float dot = 0.0f;
+    for (int64_t h = (int64_t)threadIdx.x * V; h < a.hidden; h += (int64_t)V * 256) {
+      float g[V];
+      unit_load<T, V>(dy + t * a.ld + h, g);
+      if (dweights) {
+        float v[V];
+        unit_load<T, V>(rows + (int64_t)r * a.hidden + h, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot = __builtin_fmaf(g[i], v[i], dot);
+      }
+      if (drows) {
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = w * g[i];
+        unit_store<T, V>(drows + (int64_t)r * a.hidden + h, o);
+      }
+    }
+    if (dweights) {
+      for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) dweights[t * a.topk + c] = ((part[0] + part[1]) + part[2]) + part[3];
+      __syncthreads();
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------ host side
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// calls f(element type, elements per unit) for rows of `dtype`
+template <typename F>
+void with_unit(int dtype, bool wide, F f) {
+  if (dtype == MGS_DTYPE_BF16) {
+    if (wide) f(uint16_t{}, std::integral_constant<int, 8>{});
+    else f(uint16_t{}, std::integral_constant<int, 1>{});
+  } else {
+    if (wide) f(float{}, std::integral_constant<int, 4>{});
+    else f(float{}, std::integral_constant<int, 1>{});
+  }
+}
+
+// 16-byte units need whole units per row, aligned rows and aligned tensors
+bool wide_rows(int dtype, int64_t hidden, int64_t ld, std::initializer_list<const void*> ptrs) {
+  const int n = dtype == MGS_DTYPE_BF16 ? 8 : 4;
+  if (hidden % n || ld % n) return false;
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return false;
+  return true;
+}
+
+int threads_per_token_log2(int64_t units) {
+  int k = 0;
+  while (k < 8 && ((int64_t)1 << k) < units) ++k;
+  return k;
+}
+
+int check_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, int32_t topk, const void* logits,
+                int32_t dtype, int64_t ld, RouteArgs* a) {
+  if (!rp) return fail(MGS_ERR_INVALID_ARG, "route params are NULL");
+  if (rp->score != MGS_SCORE_SOFTMAX && rp->score != MGS_SCORE_SIGMOID)
+    return fail(MGS_ERR_INVALID_ARG, "unknown score function %d", rp->score);
+  if (!(rp->scale > -3.4e38f && rp->scale < 3.4e38f)) return fail(MGS_ERR_INVALID_ARG, "scale must be finite");
+  if (experts < 1 || experts > MGS_MAX_GROUPS)
+    return fail(MGS_ERR_INVALID_ARG, "num_experts %d outside [1, %d]", experts, MGS_MAX_GROUPS);
+  if (topk < 1 || topk > MGS_MAX_TOPK || topk > experts)
+    return fail(MGS_ERR_INVALID_ARG, "topk %d outside [1, min(%d, num_experts %d)]", topk, MGS_MAX_TOPK, experts);
+  if (tokens < 0 || tokens > INT32_MAX / topk) return fail(MGS_ERR_SHAPE, "tokens %lld: tokens x topk must be in [0, 2^31)", (long long)tokens);
+  if (dtype != MGS_DTYPE_BF16 && dtype != MGS_DTYPE_F32) return fail(MGS_ERR_INVALID_ARG, "unknown logits dtype %d", dtype);
+  if (ld < experts) return fail(MGS_ERR_SHAPE, "row stride %lld below the %d experts", (long long)ld, experts);
+  if (!logits && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "logits is NULL");
+  *a = RouteArgs{tokens, experts, topk, rp->score, rp->renormalize != 0, rp->scale, ld, 0};
+  return MGS_OK;
+}
+
+int check_move(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, int64_t ld, int64_t num_rows, MoveArgs* a) {
+  if (topk < 1 || topk > MGS_MAX_TOPK) return fail(MGS_ERR_INVALID_ARG, "topk %d outside [1, %d]", topk, MGS_MAX_TOPK);
+  if (tokens < 0 || tokens > INT32_MAX / topk) return fail(MGS_ERR_SHAPE, "tokens %lld: tokens x topk must be in [0, 2^31)", (long long)tokens);
+  if (hidden < 1 || hidden > (int64_t)1 << 24) return fail(MGS_ERR_SHAPE, "hidden %lld outside [1, 2^24]", (long long)hidden);
+  if (ld < hidden) return fail(MGS_ERR_SHAPE, "row stride %lld below the width %lld", (long long)ld, (long long)hidden);
+  if (dtype != MGS_DTYPE_BF16 && dtype != MGS_DTYPE_F32) return fail(MGS_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (num_rows < 0 || num_rows > INT32_MAX) return fail(MGS_ERR_SHAPE, "num_rows %lld outside [0, 2^31)", (long long)num_rows);
+  *a = MoveArgs{tokens, hidden, ld, topk, 0, (int32_t)num_rows, 0};
+  return MGS_OK;
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MGS_ERR_HIP, "HIP launch error: %s", hipGetErrorString(e));
+  return ok();
+}
+
+template <typename F>
+void with_experts(int experts, F f) {
+  if (experts <= 16) f(std::integral_constant<int, 1>{});
+  else if (experts <= 32) f(std::integral_constant<int, 2>{});
+  else if (experts <= 64) f(std::integral_constant<int, 4>{});
+  else if (experts <= 128) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+
+}  // namespace
+}  // namespace mgs
+
+using namespace mgs;
+
+extern "C" {
+
+int mgs_moe_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, int32_t topk, const void* logits,
+                  int32_t logits_dtype, int64_t ld, int32_t* expert_idx, float* weights, void* stream) {
+  RouteArgs a;
+  int rc = check_route(rp, tokens, experts, topk, logits, logits_dtype, ld, &a);
+  if (rc) return rc;
+  if ((!expert_idx || !weights) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "expert_idx or weights is NULL");
+  if (tokens == 0) return ok();
+  const dim3 grid((unsigned)((tokens + 15) / 16));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  with_experts(experts, [&](auto n) {
+    if (logits_dtype == MGS_DTYPE_BF16)
+      hipLaunchKernelGGL((route_kernel<uint16_t, decltype(n)::value>), grid, dim3(256), 0, st, a, static_cast<const uint16_t*>(logits), expert_idx, weights);
+    else
+      hipLaunchKernelGGL((route_kernel<float, decltype(n)::value>), grid, dim3(256), 0, st, a, static_cast<const float*>(logits), expert_idx, weights);
+  });
+  return launched();
+}
+
+int mgs_moe_route_bwd(const mgs_route_params* rp, int64_t tokens, int32_t experts, int32_t topk, const void* logits,
+                      int32_t logits_dtype, int64_t ld, const int32_t* expert_idx, const float* dweights,
+                      void* dlogits, int64_t ld_dlogits, void* stream) {
+  RouteArgs a;
+  int rc = check_route(rp, tokens, experts, topk, logits, logits_dtype, ld, &a);
+  if (rc) return rc;
+  if (ld_dlogits < experts) return fail(MGS_ERR_SHAPE, "row stride %lld of dlogits below the %d experts", (long long)ld_dlogits, experts);
+  if ((!expert_idx || !dweights || !dlogits) && tokens > 0)
+    return fail(MGS_ERR_INVALID_ARG, "expert_idx, dweights or dlogits is NULL");
+  if (tokens == 0) return ok();
+  a.ldd = ld_dlogits;
+  const dim3 grid((unsigned)((tokens + 15) / 16));
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  with_experts(experts, [&](auto n) {
+    if (logits_dtype == MGS_DTYPE_BF16)
+      hipLaunchKernelGGL((route_bwd_kernel<uint16_t, decltype(n)::value>), grid, dim3(256), 0, st, a, static_cast<const uint16_t*>(logits), expert_idx, dweights, static_cast<uint16_t*>(dlogits));
+    else
+      hipLaunchKernelGGL((route_bwd_kernel<float, decltype(n)::value>), grid, dim3(256), 0, st, a, static_cast<const float*>(logits), expert_idx, dweights, static_cast<float*>(dlogits));
+  });
+  return launched();
+}
+
+int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts) {
+  if (topk < 1 || topk > MGS_MAX_TOPK) return fail(MGS_ERR_INVALID_ARG, "topk %d outside [1, %d]", topk, MGS_MAX_TOPK);
+  if (experts < 1 || experts > MGS_MAX_GROUPS)
+    return fail(MGS_ERR_INVALID_ARG, "num_experts %d outside [1, %d]", experts, MGS_MAX_GROUPS);
+  if (tokens < 0 || tokens > INT32_MAX / topk) return fail(MGS_ERR_SHAPE, "tokens %lld: tokens x topk must be in [0, 2^31)", (long long)tokens);
+  const int64_t slots = tokens * topk, chunk = sort_chunk(slots);
+  ok();
+  return 4 * std::max<int64_t>(1, (slots + chunk - 1) / chunk) * experts;
+}
+
+int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_t* expert_idx, int64_t hidden,
+                     int32_t dtype, const void* x, int64_t ldx, const float* weights, void* rows, int64_t num_rows,
+                     float* row_weights, int32_t* row_of_slot, int64_t* split_sizes, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  const int64_t need = mgs_moe_dispatch_workspace_bytes(tokens, topk, experts);
+  if (need < 0) return (int)need;
+  MoveArgs a{};
+  int rc;
+  const int64_t slots = tokens * topk;
+  if (x || rows || weights || row_weights) {
+    if ((rc = check_move(tokens, topk, hidden, dtype, ldx, num_rows, &a))) return rc;
+    if ((!x || !rows) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "x and rows go together");
+    if ((weights == nullptr) != (row_weights == nullptr))
+      return fail(MGS_ERR_INVALID_ARG, "weights and row_weights go together");
+    if (num_rows < slots)
+      return fail(MGS_ERR_SHAPE, "rows has %lld rows, %lld tokens x topk %d can need %lld", (long long)num_rows, (long long)tokens, topk, (long long)slots);
+  }
+  if (!expert_idx && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "expert_idx is NULL");
+  if (!row_of_slot && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot is NULL");
+  if (!split_sizes) return fail(MGS_ERR_INVALID_ARG, "split_sizes is NULL");
+  if (!workspace || workspace_bytes < need)
+    return fail(MGS_ERR_INVALID_ARG, "the sort needs a workspace of %lld bytes (got %lld%s)", (long long)need,
+                (long long)workspace_bytes, workspace ? "" : ", NULL");
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  const int chunk = sort_chunk(slots);
+  const dim3 grid((unsigned)std::max<int64_t>(1, (slots + chunk - 1) / chunk));
+  int32_t* counts = static_cast<int32_t*>(workspace);
+  hipLaunchKernelGGL(sort_count_kernel, grid, dim3(256), 0, st, slots, experts, chunk, expert_idx, counts);
+  hipLaunchKernelGGL(sort_rows_kernel, grid, dim3(256), 0, st, slots, experts, chunk, expert_idx, counts, row_of_slot, split_sizes);
+  if (x && tokens > 0) {
+    with_unit(dtype, wide_rows(dtype, hidden, ldx, {x, rows}), [&](auto e, auto n) {
+      typedef decltype(e) T;
+      constexpr int V = decltype(n)::value;
+      a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
+      const int64_t per = 256 >> a.tpt_log2;
+      hipLaunchKernelGGL((scatter_kernel<T, V>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a, row_of_slot,
+                         static_cast<const T*>(x), weights, static_cast<T*>(rows), row_weights);
+    });
+  }
+  return launched();
+}
+
+static int combine_call(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, const int32_t* row_of_slot,
+                        int64_t num_rows, const void* rows, const float* weights, void* y, int64_t ldy,
+                        const float* drow_weights, float* dweights, void* stream) {
+  MoveArgs a;
+  int rc = check_move(tokens, topk, hidden, dtype, ldy, num_rows, &a);
+  if (rc) return rc;
+  if ((!row_of_slot || !rows || !y) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot, the rows or the token output is NULL");
+  if ((drow_weights == nullptr) != (dweights == nullptr))
+    return fail(MGS_ERR_INVALID_ARG, "drow_weights and dweights go together");
+  if (tokens == 0) return ok();
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  with_unit(dtype, wide_rows(dtype, hidden, ldy, {rows, y}), [&](auto e, auto n) {
+    typedef decltype(e) T;
+    constexpr int V = decltype(n)::value;
+    a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
+    const int64_t per = 256 >> a.tpt_log2;
+    hipLaunchKernelGGL((combine_kernel<T, V>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a, row_of_slot,
+                       static_cast<const T*>(rows), weights, static_cast<T*>(y), drow_weights, dweights);
+  });
+  return launched();
+}
+
+int mgs_moe_combine(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, const int32_t* row_of_slot,
+                    int64_t num_rows, const void* rows, const float* weights, void* y, int64_t ldy, void* stream) {
+  return combine_call(tokens, topk, hidden, dtype, row_of_slot, num_rows, rows, weights, y, ldy, nullptr, nullptr, stream);
+}
+
+int mgs_moe_dispatch_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, const int32_t* row_of_slot,
+                         int64_t num_rows, const void* drows, const float* drow_weights, void* dx, int64_t lddx,
+                         float* dweights, void* stream) {
+  return combine_call(tokens, topk, hidden, dtype, row_of_slot, num_rows, drows, nullptr, dx, lddx, drow_weights, dweights, stream);
+}
+
+int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dtype, const int32_t* row_of_slot,
+                        int64_t num_rows, const void* dy, int64_t lddy, const void* rows, const float* weights,
+                        void* drows, float* dweights, void* stream) {
+  MoveArgs a;
+  int rc = check_move(tokens, topk, hidden, dtype, lddy, num_rows, &a);
+  if (rc) return rc;
+  if ((!row_of_slot || !dy) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot or dy is NULL");
+  if (!drows && !dweights) return fail(MGS_ERR_INVALID_ARG, "no output requested (drows and dweights are NULL)");
+  if (dweights && !rows && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "dweights needs rows, the forward's input");
+  if (tokens == 0) return ok();
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  with_unit(dtype, wide_rows(dtype, hidden, lddy, {dy, rows, drows}), [&](auto e, auto n) {
+    typedef decltype(e) T;
+    constexpr int V = decltype(n)::value;
+    hipLaunchKernelGGL((combine_bwd_kernel<T, V>), dim3((unsigned)tokens), dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(dy),
+                       static_cast<const T*>(rows), weights, static_cast<T*>(drows), dweights);
+  });
+  return launched();
+}
+
+}  // extern "C"
