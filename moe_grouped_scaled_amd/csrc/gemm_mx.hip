@@ -1190,9 +1190,9 @@ struct GemmVariant {
 };
 
 GemmVariant gemm_variant(const GemmArgs& ga, const GroupTable& gt) {
-  (void)gt;
   if (ga.fmt == MGS_FMT_MXFP8) return {gemm_mxfp8_256_kernel, BM2, BN2};
   if (ga.fmt == MGS_FMT_NVFP4) return {gemm_nvfp4_256_kernel, BM2, BN2};
+  if (ga.mode == MGS_GEMM_WGRAD || gt.total_rows > 64 * gt.num_groups) return {gemm_mxfp4_256_kernel, BM2, BN2};
   return {gemm_mxfp4_rows_kernel<4, 2>, 64, 32};
 }
 

@@ -68,6 +68,10 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
           acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[n], a[m], acc[m][n], 4, 4, 0, sb[n], 0, sa[m]);
     }
   }
+  // every path out of the loop waits the last MFMAs out before the accumulators are read
+  __builtin_amdgcn_sched_barrier(0);
+  mfma_drain();
+  __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -89,4 +93,265 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
     }
     store_values(j, row, col, v);
   }
+}
+
+// ---------------------------------------------------------------------------------- large tile
+//
+// 256 x 256 output tile per workgroup, 4 waves of 128 x 128 (4 x 4 fragments of 32 x 32, 256 FP32
+// accumulators per lane in AGPRs) on V_MFMA_SCALE_F32_32X32X64_F8F6F4, which issues faster than the
+// 16 x 16 x 128 form (8.4 against 6.3 PFLOP/s in a loop without loads).  A K step is 256 elements: 128
+// bytes a row, as in the MXFP8 kernel, whose direct-to-LDS loads, row swizzle (16-byte chunk c of row r
+// at c ^ (r & 7)) and two stages it shares.  One chunk is one scale block.
+//
+// K order inside a step: lane half h = l / 32 takes chunks 4 h .. 4 h + 3, one per 64-wide MFMA
+// (substep), the same for both operands, so its four block scales are the dword of K slice h that the
+// K-step grouped layout keeps together, and each MFMA selects its byte.
+//
+// The loop is rotated: a substep's fragments are read from LDS behind the MFMAs of the one before, and
+// the step's barrier stands before its last substep, whose fragments are in registers by then.  Behind
+// the MFMAs of that substep the next step's first fragments are read and the loads of the step after it
+// begin, so neither the LDS reads nor the barrier leave the matrix cores without work.
+constexpr int F4_KSTEP = 256;
+constexpr int F4_ROWB = F4_KSTEP / 2;
+constexpr int F4_DATA = BM2 * F4_ROWB;              // per operand and stage
+constexpr int F4_SC = BM2 * 8;                       // scale bytes per operand and stage: [K slice][row] dwords
+constexpr int F4_STAGE = 2 * (F4_DATA + F4_SC);      // A data, B data, A scales, B scales
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// acc += B . A^T for one 64-wide substep; the scale of each operand is byte KK of its dword
+template <int KK>
+__device__ __forceinline__ void mfma_scale_fp4(v16f& acc, const v4i& b, const v4i& a, uint32_t sb, uint32_t sa) {
+  if constexpr (KK == 0)
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (KK == 1)
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else if constexpr (KK == 2)
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+  else
+    asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[1,1,0] op_sel_hi:[1,1,0] cbsz:4 blgp:4"
+                 : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+
+// Epilogue: lane (r32, h32) of wave (wm, wn) holds, for fragment (fm, fn) and register group g, output row
+// 128 wm + 32 fm + r32 and the four columns 128 wn + 32 fn + 8 g + 4 h32 .. + 3.  BF16: a lane swap
+// between the halves for a pair of groups gives every lane eight consecutive columns, one 16-byte store.
+__device__ __forceinline__ void epilogue_fp4(const TileJob& j, const GemmArgs& ga, v16f (&acc)[4][4],
+                                             const uint2* bias_lds, int wm, int wn, int r32, int h32) {
+#pragma unroll
+  for (int fm = 0; fm < 4; ++fm) {
+    const int row = wm * 128 + fm * 32 + r32;
+    const bool rok = row < j.a.rows;
+    const int64_t at = (j.crow0 + row) * j.ldc + j.ccol0;
+#pragma unroll
+    for (int fn = 0; fn < 4; ++fn) {
+      const int c0 = wn * 128 + fn * 32;
+      if (!j.c32) {
+#pragma unroll
+        for (int g = 0; g < 4; g += 2) {
+          uint2 w[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint2 bw = j.bias ? bias_lds[(c0 + 8 * (g + p) + 4 * h32) >> 2] : make_uint2(0, 0);
+            const int r = 4 * (g + p);
+            float v[4];
+            frag_values(j, v4f{acc[fm][fn][r], acc[fm][fn][r + 1], acc[fm][fn][r + 2], acc[fm][fn][r + 3]}, bw, v);
+            w[p].x = bf16x2(v[0], v[1]);
+            w[p].y = bf16x2(v[2], v[3]);
+          }
+          const U2 x = swap32(w[0].x, w[1].x), y = swap32(w[0].y, w[1].y);
+          const int col = c0 + 8 * (g + h32);
+          if (rok && col < j.b.rows) st16(j.c16 + at + col, x.x, y.x, x.y, y.y);
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = c0 + 8 * g + 4 * h32;
+          const uint2 bw = j.bias ? bias_lds[col >> 2] : make_uint2(0, 0);
+          float v[4];
+          frag_values(j, v4f{acc[fm][fn][4 * g], acc[fm][fn][4 * g + 1], acc[fm][fn][4 * g + 2], acc[fm][fn][4 * g + 3]}, bw, v);
+          if (!rok || col >= j.b.rows) continue;
+          if (ga.accumulate) {
+            const float4 o = *reinterpret_cast<const float4*>(j.c32 + at + col);
+            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+          }
+          st16(j.c32 + at + col, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        }
+      }
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * F4_STAGE];
+  __shared__ __attribute__((aligned(16))) uint2 bias_lds[BN2 / 4];
+  int tile;
+  TileJob j;
+  if (tt.dev) {
+    if (!schedule_tile(*tt.dev, blockIdx.x, &tile)) return;
+    j = make_job<BM2, BN2>(ga, *tt.dev, tile);
+  } else {
+    if (!schedule_tile(tt, blockIdx.x, &tile)) return;
+    j = make_job<BM2, BN2>(ga, tt, tile);
+  }
+  if (j.k == 0) {
+    write_zero_tile<BM2, BN2>(j, ga);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, h32 = lane >> 5;
+  const TileDma d = tile_dma(j, wave, lane);
+  const uint32_t vs = (uint32_t)((wave * 64 + lane) * 4);
+
+  // load instruction n of step st into stage `stg`: 0..7 B rows, 8..15 A rows (8 rows x 128 bytes each),
+  // 16..19 the scale dwords of the wave's 64 rows (A and B, two K slices).  Rows and steps past the end
+  // read what follows or zeros: those outputs are not stored, and a partial last step is masked.
+  constexpr int NLOADS = 20;
+  auto issue_one = [&](int st, uint8_t* stg, int n) {
+    const uint32_t base = lds_addr(stg) + wave * 8 * 1024, k0 = (uint32_t)st * F4_ROWB;
+    if (n < 8) {
+      dma16(d.bd, d.vob, n * d.b_ld8 + k0, base + F4_DATA + n * 1024);
+    } else if (n < 16) {
+      dma16(d.ad, d.voa, (n - 8) * d.a_ld8 + k0, base + (n - 8) * 1024);
+    } else {
+      const uint32_t sl = (uint32_t)n & 1u, sc = lds_addr(stg) + 2 * F4_DATA + sl * (BM2 * 4) + wave * 256;
+      if (n < 18) dma4(d.bs, vs, (2u * (uint32_t)st + sl) * d.b_s4 + d.b_sr, sc + F4_SC);
+      else dma4(d.as, vs, (2u * (uint32_t)st + sl) * d.a_s4 + d.a_sr, sc);
+    }
+  };
+
+  v16f acc[4][4];
+#pragma unroll
+  for (int fm = 0; fm < 4; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < 4; ++fn) acc[fm][fn] = v16f{};
+  __builtin_amdgcn_sched_barrier(0);
+  mfma_valu_gap();
+  __builtin_amdgcn_sched_barrier(0);
+
+  // fragment f of the wave's 128 rows: row 128 w + 32 f + r32; rows 32 f apart share the chunk swizzle
+  const uint32_t ra = (uint32_t)(wm * 128 + r32) * F4_ROWB, rb = (uint32_t)(wn * 128 + r32) * F4_ROWB + F4_DATA;
+  const uint32_t sa0 = 2 * F4_DATA + h32 * (BM2 * 4) + (wm * 128 + r32) * 4, sb0 = sa0 + F4_SC + (wn - wm) * 512;
+  auto frag = [&](const uint8_t* stg, uint32_t row, int f, int kk) {
+    return *reinterpret_cast<const v4i*>(stg + row + f * 32 * F4_ROWB + (((4 * h32 + kk) ^ (r32 & 7)) << 4));
+  };
+  v4i fa[2][4], fb[2][4];          // fragments of the even and odd substeps
+  uint32_t sa[4], sb[4], na[4], nb[4];  // scale dwords of this step and the next
+  // read i (0..7) of substep kk: B fragments, then A; read 8..15 the step's scales
+  auto read_one = [&](const uint8_t* stg, int kk, int buf, int i) {
+    if (i < 4) fb[buf][i] = frag(stg, rb, i, kk);
+    else if (i < 8) fa[buf][i - 4] = frag(stg, ra, i - 4, kk);
+    else if (i < 12) nb[i - 8] = *reinterpret_cast<const uint32_t*>(stg + sb0 + (i - 8) * 128);
+    else na[i - 12] = *reinterpret_cast<const uint32_t*>(stg + sa0 + (i - 12) * 128);
+  };
+
+  const int nsteps = __builtin_amdgcn_readfirstlane((int)((j.k + F4_KSTEP - 1) / F4_KSTEP));
+  const int last_rem = (int)(j.k - (int64_t)(nsteps - 1) * F4_KSTEP);
+
+  // the 16 MFMAs of substep KK from fragment buffer KK % 2, `behind(m)` after the m-th
+  auto substep = [&](auto kk, auto&& behind) {
+    constexpr int KK = decltype(kk)::value, B = KK & 1;
+#pragma unroll
+    for (int fm = 0; fm < 4; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < 4; ++fn) {
+        mfma_scale_fp4<KK>(acc[fm][fn], fb[B][fn], fa[B][fm], sb[fn], sa[fm]);
+        behind(4 * fm + fn);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  // K elements past the end of the reduction: zero codes with the scale code 0
+  auto mask = [&](int kk) {
+    const int left = last_rem - 128 * h32;                // the lane's part of the step
+    const bool ok = 32 * kk < left;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        fa[kk & 1][f][t] = ok ? fa[kk & 1][f][t] : 0;
+        fb[kk & 1][f][t] = ok ? fb[kk & 1][f][t] : 0;
+      }
+      asm volatile("" : "+v"(fa[kk & 1][f]), "+v"(fb[kk & 1][f]));
+      if (kk == 0) {
+        const uint32_t m = left >= 128 ? 0xffffffffu : left <= 0 ? 0u : (1u << (left >> 2)) - 1u;  // 8 bits per 32 elements
+        sa[f] &= m;
+        sb[f] &= m;
+        asm volatile("" : "+v"(sa[f]), "+v"(sb[f]));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_valu_gap();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr std::integral_constant<int, 0> K0{};
+  constexpr std::integral_constant<int, 1> K1{};
+  constexpr std::integral_constant<int, 2> K2{};
+  constexpr std::integral_constant<int, 3> K3{};
+  // One K step.  The loads of step st + 1 (their first LEAD were issued in the step before) go out one per
+  // PACE MFMAs.
+  constexpr int PACE = 2, LEAD = 16 / PACE;
+  auto step = [&](auto tail_tag, int st) {
+    constexpr bool TAIL = decltype(tail_tag)::value;
+    uint8_t* stg = smem + (st & 1) * F4_STAGE;
+    uint8_t* nxt = smem + ((st + 1) & 1) * F4_STAGE;
+    const bool more = !TAIL && st + 1 < nsteps, more2 = !TAIL && st + 2 < nsteps;
+    auto feed = [&](int m) {  // m-th MFMA of the step's first three substeps
+      if (more && m % PACE == PACE - 1 && LEAD + m / PACE < NLOADS) issue_one(st + 1, nxt, LEAD + m / PACE);
+    };
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      sa[f] = na[f];
+      sb[f] = nb[f];
+      asm volatile("" : "+v"(sa[f]), "+v"(sb[f]));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_valu_gap();
+    __builtin_amdgcn_sched_barrier(0);
+    if (TAIL) mask(0);
+    substep(K0, [&](int m) { if (m < 8) read_one(stg, 1, 1, m); feed(m); });
+    if (TAIL) mask(1);
+    substep(K1, [&](int m) { if (m < 8) read_one(stg, 2, 0, m); feed(16 + m); });
+    if (TAIL) mask(2);
+    substep(K2, [&](int m) { if (m < 8) read_one(stg, 3, 1, m); feed(32 + m); });
+    if (TAIL) mask(3);
+    // from here on the other stage is loaded and this one read by every wave
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    substep(K3, [&](int m) {
+      if (more) {
+        if (m < 8) read_one(nxt, 0, 0, m);
+        else if (m < 12) { read_one(nxt, 0, 0, 2 * m - 8); read_one(nxt, 0, 0, 2 * m - 7); }
+      }
+      if (more2 && m % PACE == PACE - 1) issue_one(st + 2, stg, m / PACE);
+    });
+    // the tile's last MFMAs are waited out on each path (accumulator copies may follow the join)
+    if (!more) {
+      __builtin_amdgcn_sched_barrier(0);
+      mfma_drain();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  for (int n = 0; n < NLOADS; ++n) issue_one(0, smem, n);
+  if (d.has_bias && wave < 2) dma4(d.bias, (uint32_t)(wave * 256 + lane * 4), 0, lds_addr(bias_lds) + wave * 256);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) read_one(smem, 0, 0, i);
+  if (nsteps > 1)
+    for (int n = 0; n < LEAD; ++n) issue_one(1, smem + F4_STAGE, n);
+  const bool tail = last_rem < F4_KSTEP;
+  const int full = tail ? nsteps - 1 : nsteps;
+  for (int st = 0; st < full; ++st) step(std::false_type{}, st);
+  if (tail) step(std::true_type{}, nsteps - 1);
+  __builtin_amdgcn_sched_barrier(0);
+  mfma_drain();
+  __builtin_amdgcn_sched_barrier(0);
+  epilogue_fp4(j, ga, acc, bias_lds, wm, wn, r32, h32);
 }
