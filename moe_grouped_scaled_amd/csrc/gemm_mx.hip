@@ -71,7 +71,9 @@ constexpr int TILE_BLOCK_N = 4;
 //   FPROP B:         rowwise qtensor [E * n x k]             (scale matrix: all E * n rows)
 //   DGRAD B:         columnwise qtensor of an [E * k x n] weight: per group [n x kp], kp = roundup(k, 128)
 //   WGRAD A / B:     columnwise qtensors of widths m / n: per group [m x mp_g] / [n x mp_g]
-template <int TM, int TN, typename Table>
+// The format is a template parameter: with elements per byte and per scale as run-time values the 64-bit
+// divisions by them were ~2500 scalar instructions before a tile's first load.
+template <int FMT, int TM, int TN, typename Table>
 __device__ __forceinline__ TileJob make_job(const GemmArgs& ga, const Table& tt, int tile) {
   int lo = 0, hi = tt.num_groups;  // tile_off[lo] <= tile < tile_off[hi]
   while (hi - lo > 1) {
@@ -82,9 +84,9 @@ __device__ __forceinline__ TileJob make_job(const GemmArgs& ga, const Table& tt,
   const int g = lo;
   j.g = g;
   const int lt = tile - tt.tile_off[g];
-  const bool nv = ga.fmt == MGS_FMT_NVFP4;
-  const int ediv = ga.fmt == MGS_FMT_MXFP8 ? 1 : 2;  // elements per byte
-  const int sblk = nv ? 16 : 32;          // elements per scale
+  constexpr bool nv = FMT == MGS_FMT_NVFP4;
+  constexpr unsigned ediv = FMT == MGS_FMT_MXFP8 ? 1 : 2;  // elements per byte
+  constexpr unsigned sblk = nv ? 16 : 32;                  // elements per scale
   // Tiles of a group run in column blocks of TILE_BLOCK_N tile columns, row-major inside a block:
   // the workgroups in flight on one XCD (dispatched together) then share each K slice of A with
   // TILE_BLOCK_N tiles and each K slice of B with all tile rows of the block, which keeps the slices
@@ -177,7 +179,14 @@ __device__ __forceinline__ TileJob make_job(const GemmArgs& ga, const Table& tt,
   j.ccol0 = brow0;
   j.a.rows = (int)min<int64_t>(TM, arows_total);
   j.b.rows = (int)min<int64_t>(TN, ga.n - brow0);
-  j.gfactor = nv ? ga.a_gscale[g] * ga.b_gscale[g] : 1.0f;
+  if constexpr (nv) {
+    j.gfactor = ga.a_gscale[g] * ga.b_gscale[g];
+  } else {
+    // a factor the compiler cannot fold: without the multiplication it copied the MXFP8 kernel's
+    // accumulator array to scratch ahead of the wait for the last MFMAs
+    j.gfactor = 1.0f;
+    asm("" : "+s"(j.gfactor));
+  }
   return j;
 }
 
@@ -565,10 +574,10 @@ void gemm_mxfp8_256_kernel(GemmArgs ga, GemmTable tt) {
   TileJob j;
   if (tt.dev) {
     if (!schedule_tile(*tt.dev, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, *tt.dev, tile);
+    j = make_job<MGS_FMT_MXFP8, BM2, BN2>(ga, *tt.dev, tile);
   } else {
     if (!schedule_tile(tt, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, tt, tile);
+    j = make_job<MGS_FMT_MXFP8, BM2, BN2>(ga, tt, tile);
   }
   if (j.k == 0) {
     write_zero_tile<BM2, BN2>(j, ga);
@@ -829,10 +838,10 @@ void gemm_nvfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   TileJob j;
   if (tt.dev) {
     if (!schedule_tile(*tt.dev, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, *tt.dev, tile);
+    j = make_job<MGS_FMT_NVFP4, BM2, BN2>(ga, *tt.dev, tile);
   } else {
     if (!schedule_tile(tt, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, tt, tile);
+    j = make_job<MGS_FMT_NVFP4, BM2, BN2>(ga, tt, tile);
   }
   if (j.k == 0) {
     write_zero_tile<BM2, BN2>(j, ga);

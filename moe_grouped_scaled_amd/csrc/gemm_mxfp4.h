@@ -23,10 +23,10 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
   TileJob j;
   if (tt.dev) {
     if (!schedule_tile(*tt.dev, blockIdx.x, &tile)) return;
-    j = make_job<TM, TN>(ga, *tt.dev, tile);
+    j = make_job<MGS_FMT_MXFP4, TM, TN>(ga, *tt.dev, tile);
   } else {
     if (!schedule_tile(tt, blockIdx.x, &tile)) return;
-    j = make_job<TM, TN>(ga, tt, tile);
+    j = make_job<MGS_FMT_MXFP4, TM, TN>(ga, tt, tile);
   }
   if (j.k == 0) {
     write_zero_tile<TM, TN>(j, ga);
@@ -100,8 +100,10 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
 // 256 x 256 output tile per workgroup, 4 waves of 128 x 128 (4 x 4 fragments of 32 x 32, 256 FP32
 // accumulators per lane in AGPRs) on V_MFMA_SCALE_F32_32X32X64_F8F6F4, which issues faster than the
 // 16 x 16 x 128 form (8.4 against 6.3 PFLOP/s in a loop without loads).  A K step is 256 elements: 128
-// bytes a row, as in the MXFP8 kernel, whose direct-to-LDS loads, row swizzle (16-byte chunk c of row r
-// at c ^ (r & 7)) and two stages it shares.  One chunk is one scale block.
+// bytes a row, as in the MXFP8 kernel, whose direct-to-LDS loads and two stages it shares.  One 16-byte
+// chunk is one scale block; chunk c of row r is stored at c ^ ((r >> 1) & 7), which keeps the 32-row
+// fragment reads free of bank conflicts (with the MXFP8 kernel's r & 7, made for 16-row fragments, the
+// conflicts counted were 0.47 of the LDS cycles).
 //
 // K order inside a step: lane half h = l / 32 takes chunks 4 h .. 4 h + 3, one per 64-wide MFMA
 // (substep), the same for both operands, so its four block scales are the dword of K slice h that the
@@ -139,46 +141,50 @@ __device__ __forceinline__ void mfma_scale_fp4(v16f& acc, const v4i& b, const v4
 // Epilogue: lane (r32, h32) of wave (wm, wn) holds, for fragment (fm, fn) and register group g, output row
 // 128 wm + 32 fm + r32 and the four columns 128 wn + 32 fn + 8 g + 4 h32 .. + 3.  BF16: a lane swap
 // between the halves for a pair of groups gives every lane eight consecutive columns, one 16-byte store.
-__device__ __forceinline__ void epilogue_fp4(const TileJob& j, const GemmArgs& ga, v16f (&acc)[4][4],
-                                             const uint2* bias_lds, int wm, int wn, int r32, int h32) {
+// Whole fragments are in or out by column (N % 32 == 0), rows are masked once per fragment row, and the
+// addresses are a wave-uniform base and one 32-bit lane offset.
+template <bool F32, bool ACC, bool BIAS>
+__device__ __forceinline__ void epilogue_fp4(const TileJob& j, v16f (&acc)[4][4], const uint2* bias_lds, int wm, int wn,
+                                             int r32, int h32) {
+  const uint32_t lane_off = (uint32_t)r32 * (uint32_t)j.ldc + (F32 ? 4u : 8u) * (uint32_t)h32;
 #pragma unroll
   for (int fm = 0; fm < 4; ++fm) {
-    const int row = wm * 128 + fm * 32 + r32;
-    const bool rok = row < j.a.rows;
-    const int64_t at = (j.crow0 + row) * j.ldc + j.ccol0;
+    const int row0 = wm * 128 + fm * 32;
+    if (row0 + r32 >= j.a.rows) continue;
+    const int64_t base = (j.crow0 + row0) * j.ldc + j.ccol0;
 #pragma unroll
     for (int fn = 0; fn < 4; ++fn) {
       const int c0 = wn * 128 + fn * 32;
-      if (!j.c32) {
+      if (c0 >= j.b.rows) continue;
+      float v[4][4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[g][t] = acc[fm][fn][4 * g + t];
+        if constexpr (BIAS) {
+          const uint2 bw = bias_lds[(c0 + 8 * g + 4 * h32) >> 2];
+          v[g][0] += bf16lo(bw.x); v[g][1] += bf16hi(bw.x); v[g][2] += bf16lo(bw.y); v[g][3] += bf16hi(bw.y);
+        }
+      }
+      if constexpr (F32) {
+        float* p = j.c32 + base + c0;
+        float4 o[4];
+        if constexpr (ACC) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) o[g] = *reinterpret_cast<const float4*>(p + lane_off + 8 * g);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) { v[g][0] += o[g].x; v[g][1] += o[g].y; v[g][2] += o[g].z; v[g][3] += o[g].w; }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          st16(p + lane_off + 8 * g, __float_as_uint(v[g][0]), __float_as_uint(v[g][1]), __float_as_uint(v[g][2]), __float_as_uint(v[g][3]));
+      } else {
+        uint16_t* p = j.c16 + base + c0;
 #pragma unroll
         for (int g = 0; g < 4; g += 2) {
-          uint2 w[2];
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const uint2 bw = j.bias ? bias_lds[(c0 + 8 * (g + p) + 4 * h32) >> 2] : make_uint2(0, 0);
-            const int r = 4 * (g + p);
-            float v[4];
-            frag_values(j, v4f{acc[fm][fn][r], acc[fm][fn][r + 1], acc[fm][fn][r + 2], acc[fm][fn][r + 3]}, bw, v);
-            w[p].x = bf16x2(v[0], v[1]);
-            w[p].y = bf16x2(v[2], v[3]);
-          }
-          const U2 x = swap32(w[0].x, w[1].x), y = swap32(w[0].y, w[1].y);
-          const int col = c0 + 8 * (g + h32);
-          if (rok && col < j.b.rows) st16(j.c16 + at + col, x.x, y.x, x.y, y.y);
-        }
-      } else {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = c0 + 8 * g + 4 * h32;
-          const uint2 bw = j.bias ? bias_lds[col >> 2] : make_uint2(0, 0);
-          float v[4];
-          frag_values(j, v4f{acc[fm][fn][4 * g], acc[fm][fn][4 * g + 1], acc[fm][fn][4 * g + 2], acc[fm][fn][4 * g + 3]}, bw, v);
-          if (!rok || col >= j.b.rows) continue;
-          if (ga.accumulate) {
-            const float4 o = *reinterpret_cast<const float4*>(j.c32 + at + col);
-            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
-          }
-          st16(j.c32 + at + col, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+          const U2 x = swap32(bf16x2(v[g][0], v[g][1]), bf16x2(v[g + 1][0], v[g + 1][1]));
+          const U2 y = swap32(bf16x2(v[g][2], v[g][3]), bf16x2(v[g + 1][2], v[g + 1][3]));
+          st16(p + lane_off + 8 * g, x.x, y.x, x.y, y.y);
         }
       }
     }
@@ -193,10 +199,10 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   TileJob j;
   if (tt.dev) {
     if (!schedule_tile(*tt.dev, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, *tt.dev, tile);
+    j = make_job<MGS_FMT_MXFP4, BM2, BN2>(ga, *tt.dev, tile);
   } else {
     if (!schedule_tile(tt, blockIdx.x, &tile)) return;
-    j = make_job<BM2, BN2>(ga, tt, tile);
+    j = make_job<MGS_FMT_MXFP4, BM2, BN2>(ga, tt, tile);
   }
   if (j.k == 0) {
     write_zero_tile<BM2, BN2>(j, ga);
@@ -208,6 +214,12 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   const int r32 = lane & 31, h32 = lane >> 5;
   const TileDma d = tile_dma(j, wave, lane);
   const uint32_t vs = (uint32_t)((wave * 64 + lane) * 4);
+  // lane offset of the loads of 8-row groups n (even, odd): row 64 wave + 8 n + lane / 8, the chunk that
+  // belongs at position lane % 8
+  const int lrow = lane >> 3;
+  const uint32_t lsw = (uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4);
+  const uint32_t va0 = (uint32_t)((wave * 64 + lrow) * j.a.ld), vb0 = (uint32_t)((wave * 64 + lrow) * j.b.ld);
+  const uint32_t voa[2] = {va0 + lsw, va0 + (lsw ^ 64u)}, vob[2] = {vb0 + lsw, vb0 + (lsw ^ 64u)};
 
   // load instruction n of step st into stage `stg`: 0..7 B rows, 8..15 A rows (8 rows x 128 bytes each),
   // 16..19 the scale dwords of the wave's 64 rows (A and B, two K slices).  Rows and steps past the end
@@ -216,9 +228,9 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   auto issue_one = [&](int st, uint8_t* stg, int n) {
     const uint32_t base = lds_addr(stg) + wave * 8 * 1024, k0 = (uint32_t)st * F4_ROWB;
     if (n < 8) {
-      dma16(d.bd, d.vob, n * d.b_ld8 + k0, base + F4_DATA + n * 1024);
+      dma16(d.bd, vob[n & 1], n * d.b_ld8 + k0, base + F4_DATA + n * 1024);
     } else if (n < 16) {
-      dma16(d.ad, d.voa, (n - 8) * d.a_ld8 + k0, base + (n - 8) * 1024);
+      dma16(d.ad, voa[n & 1], (n - 8) * d.a_ld8 + k0, base + (n - 8) * 1024);
     } else {
       const uint32_t sl = (uint32_t)n & 1u, sc = lds_addr(stg) + 2 * F4_DATA + sl * (BM2 * 4) + wave * 256;
       if (n < 18) dma4(d.bs, vs, (2u * (uint32_t)st + sl) * d.b_s4 + d.b_sr, sc + F4_SC);
@@ -239,7 +251,7 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   const uint32_t ra = (uint32_t)(wm * 128 + r32) * F4_ROWB, rb = (uint32_t)(wn * 128 + r32) * F4_ROWB + F4_DATA;
   const uint32_t sa0 = 2 * F4_DATA + h32 * (BM2 * 4) + (wm * 128 + r32) * 4, sb0 = sa0 + F4_SC + (wn - wm) * 512;
   auto frag = [&](const uint8_t* stg, uint32_t row, int f, int kk) {
-    return *reinterpret_cast<const v4i*>(stg + row + f * 32 * F4_ROWB + (((4 * h32 + kk) ^ (r32 & 7)) << 4));
+    return *reinterpret_cast<const v4i*>(stg + row + f * 32 * F4_ROWB + (((4 * h32 + kk) ^ ((r32 >> 1) & 7)) << 4));
   };
   v4i fa[2][4], fb[2][4];          // fragments of the even and odd substeps
   uint32_t sa[4], sb[4], na[4], nb[4];  // scale dwords of this step and the next
@@ -338,6 +350,7 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
     }
   };
 
+#pragma unroll
   for (int n = 0; n < NLOADS; ++n) issue_one(0, smem, n);
   if (d.has_bias && wave < 2) dma4(d.bias, (uint32_t)(wave * 256 + lane * 4), 0, lds_addr(bias_lds) + wave * 256);
   __builtin_amdgcn_s_waitcnt(0);
@@ -345,6 +358,7 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) read_one(smem, 0, 0, i);
   if (nsteps > 1)
+#pragma unroll
     for (int n = 0; n < LEAD; ++n) issue_one(1, smem + F4_STAGE, n);
   const bool tail = last_rem < F4_KSTEP;
   const int full = tail ? nsteps - 1 : nsteps;
@@ -353,5 +367,14 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   __builtin_amdgcn_sched_barrier(0);
   mfma_drain();
   __builtin_amdgcn_sched_barrier(0);
-  epilogue_fp4(j, ga, acc, bias_lds, wm, wn, r32, h32);
+  if (!j.c32) {
+    if (d.has_bias) epilogue_fp4<false, false, true>(j, acc, bias_lds, wm, wn, r32, h32);
+    else epilogue_fp4<false, false, false>(j, acc, bias_lds, wm, wn, r32, h32);
+  } else if (d.has_bias) {
+    if (ga.accumulate) epilogue_fp4<true, true, true>(j, acc, bias_lds, wm, wn, r32, h32);
+    else epilogue_fp4<true, false, true>(j, acc, bias_lds, wm, wn, r32, h32);
+  } else {
+    if (ga.accumulate) epilogue_fp4<true, true, false>(j, acc, bias_lds, wm, wn, r32, h32);
+    else epilogue_fp4<true, false, false>(j, acc, bias_lds, wm, wn, r32, h32);
+  }
 }
