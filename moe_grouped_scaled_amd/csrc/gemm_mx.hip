@@ -1030,14 +1030,6 @@ void gemm_nvfp4_256_kernel(GemmArgs ga, GemmTable tt) {
 
 // ------------------------------------------------------------------------------------ MXFP4 path
 
-// raw buffer view of `bytes` bytes at `p` for the compiler's buffer loads (p and bytes wave-uniform)
-typedef __amdgpu_buffer_rsrc_t fp4_view_t;
-__device__ __forceinline__ fp4_view_t fp4_view(const uint8_t* p, int64_t bytes) {
-  const sdesc_t d = gemm_view(p, bytes);
-  const uint64_t a = (uint64_t)(uint32_t)d[0] | ((uint64_t)(uint32_t)d[1] << 32);
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a), 0, d[2], RSRC_WORD3);
-}
-
 #include "gemm_mxfp4.h"
 
 }  // namespace
@@ -1198,11 +1190,56 @@ struct GemmVariant {
   int tm, tn;
 };
 
+// Tiles of a launch with tm x tn tiles; with device-resident split sizes a bound.
+int64_t count_tiles(const GemmArgs& ga, const GroupTable& gt, int tm, int tn) {
+  const int64_t ntn = (ga.n + tn - 1) / tn;
+  int64_t rows = 0;
+  if (ga.mode == MGS_GEMM_WGRAD) {
+    rows = (ga.m + tm - 1) / tm * gt.num_groups;
+  } else if (gt.dev) {
+    rows = ((int64_t)gt.total_rows + tm - 1) / tm + gt.num_groups;
+  } else {
+    for (int g = 0; g < gt.num_groups; ++g) rows += (gt.row_off[g + 1] - gt.row_off[g] + tm - 1) / tm;
+  }
+  return rows * ntn;
+}
+
+// MXFP4: which kernel and tile.  The 256 x 256 kernel needs tiles for half the CUs at least and groups of
+// more than 64 rows; below, a tile's time (26 us at K = 4096) stands alone: one expert x 256 rows, 4096 x
+// 4096 takes 28.9 us with it and 9.8 us in 512 tiles of 32 x 64, 1024 rows 29.7 and 22.3 us (64 x 64); 16
+// experts x 128 rows (256 tiles) 48.9 and 58 us; 16 experts x 64 rows 44.7 and 42.1 us.  The few-rows
+// kernel takes the largest tile that still gives two workgroups per CU: 64 x 64 reads the weights once
+// for 64 rows, smaller ones fill the chip (one expert x 64 rows: 9.9 us in 64 x 64, 6.1 us in 32 x 32), and
+// no taller tile than the largest group needs (16 experts x 2 rows: 30.8 us with 16 x 32, 35.9 with 64 x 64).
+// Its ring holds two units where there are few workgroups (one expert x 1 row, 8192 x 8192: 8.8 against 10.2
+// us with one), one where several workgroups per CU hide each other's loads (32 experts x 1 row, 7168 x
+// 2048: 45.8 against 56.4 us with two).  With device-resident split sizes the host knows the capacity only:
+// the largest group is taken to have twice the mean, and any other routing is right, if slower.
+GemmVariant mxfp4_variant(const GemmArgs& ga, const GroupTable& gt) {
+  int64_t most = 0;
+  if (ga.mode == MGS_GEMM_WGRAD) {
+    most = ga.m;
+  } else if (gt.dev) {
+    most = std::min<int64_t>(gt.total_rows, std::max<int64_t>(16, 2 * (int64_t)gt.total_rows / gt.num_groups));
+  } else {
+    for (int g = 0; g < gt.num_groups; ++g) most = std::max<int64_t>(most, gt.row_off[g + 1] - gt.row_off[g]);
+  }
+  if (most > 64 && count_tiles(ga, gt, BM2, BN2) > 128) return {gemm_mxfp4_256_kernel, BM2, BN2};
+  const int64_t fill = 512;
+  if (most <= 16) {
+    if (count_tiles(ga, gt, 16, 32) >= fill) return {gemm_mxfp4_rows_kernel<1, 2, 1>, 16, 32};
+    return {gemm_mxfp4_rows_kernel<1, 2, 2>, 16, 32};
+  }
+  if (most > 32 && count_tiles(ga, gt, 64, 64) >= fill) return {gemm_mxfp4_rows_kernel<4, 4, 1>, 64, 64};
+  if (count_tiles(ga, gt, 32, 64) >= fill) return {gemm_mxfp4_rows_kernel<2, 4, 1>, 32, 64};
+  if (count_tiles(ga, gt, 32, 32) >= fill) return {gemm_mxfp4_rows_kernel<2, 2, 1>, 32, 32};
+  return {gemm_mxfp4_rows_kernel<2, 2, 2>, 32, 32};
+}
+
 GemmVariant gemm_variant(const GemmArgs& ga, const GroupTable& gt) {
   if (ga.fmt == MGS_FMT_MXFP8) return {gemm_mxfp8_256_kernel, BM2, BN2};
   if (ga.fmt == MGS_FMT_NVFP4) return {gemm_nvfp4_256_kernel, BM2, BN2};
-  if (ga.mode == MGS_GEMM_WGRAD || gt.total_rows > 64 * gt.num_groups) return {gemm_mxfp4_256_kernel, BM2, BN2};
-  return {gemm_mxfp4_rows_kernel<4, 2>, 64, 32};
+  return mxfp4_variant(ga, gt);
 }
 
 }  // namespace
@@ -1210,13 +1247,7 @@ GemmVariant gemm_variant(const GemmArgs& ga, const GroupTable& gt) {
 int64_t gemm_tile_count(const GemmArgs& ga, const GroupTable& gt) {
   const GemmVariant v = gemm_variant(ga, gt);
   if (gt.dev) return capacity_grid(ga, gt, v.tm, v.tn);
-  int64_t rows = 0;
-  if (ga.mode == MGS_GEMM_WGRAD) {
-    rows = (ga.m + v.tm - 1) / v.tm * gt.num_groups;
-  } else {
-    for (int g = 0; g < gt.num_groups; ++g) rows += (gt.row_off[g + 1] - gt.row_off[g] + v.tm - 1) / v.tm;
-  }
-  return rows * ((ga.n + v.tn - 1) / v.tn);
+  return count_tiles(ga, gt, v.tm, v.tn);
 }
 
 hipError_t launch_gemm(const GemmArgs& ga, const GroupTable& gt, hipStream_t st, GemmTable* dev_gemm_table) {

@@ -12,13 +12,31 @@
 // ---------------------------------------------------------------------------------- few rows
 //
 // A workgroup owns 16 MT rows x 16 NT columns of one group; its four waves split K: wave w takes the
-// 256-element units w, w + 4, ... (a unit of a row is one 128-byte line), and the four partial tiles
-// are added in wave order through LDS, so the result does not depend on timing.  Operands go from
-// global memory to registers, no LDS staging: with few rows every weight is used by one workgroup only.
-template <int MT, int NT>
+// 256-element units w, w + 4, ... and the four partial tiles are added in wave order through LDS, so the
+// result does not depend on timing.  With few rows the time is that of reading the weights once, so what
+// counts is bytes in flight: every wave has its own ring of D units in LDS, filled by direct-to-LDS loads
+// (eight lanes read a row's 128-byte line; reading fragments from global memory straight into registers,
+// four rows per lane quad, reached 4.0 TB/s), and waits for the oldest unit only.  Waves share nothing
+// until the end: no barrier in the loop.  Units past the end are loaded masked (no memory traffic), which
+// keeps the count of loads in flight, and with it the wait, the same for every unit.
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr int rows_scale_loads(int frags) { return (32 * frags + 63) / 64; }  // dword loads, 64 lanes each
+constexpr int rows_unit_bytes(int mt, int nt) {
+  return (mt + nt) * 2048 + (rows_scale_loads(mt) + rows_scale_loads(nt)) * 256;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+template <int MT, int NT, int D>
 __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmTable tt) {
   constexpr int TM = 16 * MT, TN = 16 * NT, WAVES = 4;
-  __shared__ float part[WAVES][TM][TN + 4];
+  constexpr int SM = rows_scale_loads(MT), SN = rows_scale_loads(NT), UNIT = rows_unit_bytes(MT, NT);
+  constexpr int LOADS = 2 * (MT + NT) + SM + SN;  // per unit
+  constexpr int PITCH = TN + 4;
+  constexpr int RING = WAVES * D * UNIT, PART = WAVES * TM * PITCH * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PART ? RING : PART];
   int tile;
   TileJob j;
   if (tt.dev) {
@@ -34,40 +52,89 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
   }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
-  const fp4_view_t av = fp4_view(j.a.data, j.a.avail), bv = fp4_view(j.b.data, j.b.avail);
-  const fp4_view_t asv = fp4_view(j.a.sbase, j.a.savail), bsv = fp4_view(j.b.sbase, j.b.savail);
+  const int nblk = __builtin_amdgcn_readfirstlane((int)(j.k >> 5));  // 32-element K blocks (k % 32 == 0)
+  const int nslices = (nblk + 3) >> 2;
+  const sdesc_t ad = gemm_view(j.a.data, j.a.avail), bd = gemm_view(j.b.data, j.b.avail);
+  const sdesc_t as = gemm_view(j.a.sbase, j.a.savail), bs = gemm_view(j.b.sbase, j.b.savail);
+  const uint32_t as4 = __builtin_amdgcn_readfirstlane((uint32_t)j.a.srows * 4u), bs4 = __builtin_amdgcn_readfirstlane((uint32_t)j.b.srows * 4u);
+  constexpr uint32_t OUT = 0x80000000u;  // past every record count: reads as zero, no memory access
+  // data load: row 8 i + lane / 8 of a fragment set, the chunk that belongs at position lane % 8
+  const int lrow = lane >> 3, chunk = (lane & 7) ^ lrow;
+  const uint32_t ald = (uint32_t)j.a.ld, bld = (uint32_t)j.b.ld;
+  uint8_t* ring = smem + wave * D * UNIT;
+  const uint32_t ring_at = lds_addr(ring);
+  auto issue = [&](int i) {  // the wave's i-th unit into slot i % D
+    const int u = wave + WAVES * i;
+    const uint32_t base = ring_at + (uint32_t)(i % D) * UNIT;
+    const bool cok = 8 * u + chunk < nblk;
+    const uint32_t k0 = 128u * (uint32_t)u + 16u * (uint32_t)chunk;
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) {
+      const int r = 8 * n + lrow;
+      dma16(bd, cok && r < j.b.rows ? (uint32_t)r * bld + k0 : OUT, 0, base + n * 1024);
+    }
+#pragma unroll
+    for (int n = 0; n < SN; ++n) {
+      const int x = 64 * n + lane, sl = x / TN, r = x - sl * TN;
+      const bool ok = sl < 2 && 2 * u + sl < nslices && r < j.b.rows;
+      dma4(bs, ok ? (uint32_t)(2 * u + sl) * bs4 + ((uint32_t)j.b.srow0 + (uint32_t)r) * 4u : OUT, 0, base + NT * 2048 + n * 256);
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * MT; ++n) {
+      const int r = 8 * n + lrow;
+      dma16(ad, cok && r < j.a.rows ? (uint32_t)r * ald + k0 : OUT, 0, base + NT * 2048 + SN * 256 + n * 1024);
+    }
+#pragma unroll
+    for (int n = 0; n < SM; ++n) {
+      const int x = 64 * n + lane, sl = x / TM, r = x - sl * TM;
+      const bool ok = sl < 2 && 2 * u + sl < nslices && r < j.a.rows;
+      dma4(as, ok ? (uint32_t)(2 * u + sl) * as4 + ((uint32_t)j.a.srow0 + (uint32_t)r) * 4u : OUT, 0,
+           base + (NT + MT) * 2048 + SN * 256 + n * 256);
+    }
+  };
   v4f acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const int nblk = (int)(j.k >> 5);  // 32-element K blocks (k % 32 == 0)
-  // the lane's data of fragment row r and K block kb, and its scale; rows past the tile's end and
-  // blocks past the end of K read as zero codes with a zero (finite) scale
-  auto load = [&](const fp4_view_t& d, const fp4_view_t& s, const Operand& o, int r, int kb, v8i& v, int& sc) {
-    const bool ok = r < o.rows && kb < nblk;
-    const v4u w = __builtin_amdgcn_raw_buffer_load_b128(d, ok ? r * (int)o.ld + kb * 16 : (int)0x80000000u, 0, 0);
-    v = v8i{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-    const uint32_t so = ((uint32_t)(kb >> 2) * (uint32_t)o.srows + (uint32_t)o.srow0 + (uint32_t)r) * 4u + (uint32_t)(kb & 3);
-    sc = __builtin_amdgcn_raw_buffer_load_b8(s, ok ? (int)so : (int)0x80000000u, 0, 0);
-  };
-  for (int u = wave; 8 * u < nblk; u += WAVES) {
+  const int nu = __builtin_amdgcn_readfirstlane(((nblk + 7) / 8 - wave + WAVES - 1) / WAVES);  // the wave's units
+#pragma unroll
+  for (int i = 0; i < D; ++i) issue(i);
+  for (int i = 0; i < nu; ++i) {
+    wait_loads<(D - 1) * LOADS>();
+    const uint8_t* pb = ring + (i % D) * UNIT;
+    const uint8_t* pa = pb + NT * 2048 + SN * 256;
+    const uint8_t *psb = pb + NT * 2048, *psa = pa + MT * 2048;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int kb = 8 * u + 4 * h + q;
+      const int at = ((4 * h + q) ^ (r16 & 7)) << 4;
       v8i a[MT], b[NT];
       int sa[MT], sb[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) load(bv, bsv, j.b, 16 * n + r16, kb, b[n], sb[n]);
+      for (int n = 0; n < NT; ++n) {
+        const v4i w = *reinterpret_cast<const v4i*>(pb + (16 * n + r16) * 128 + at);
+        b[n] = v8i{w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+        sb[n] = psb[(h * TN + 16 * n + r16) * 4 + q];
+      }
 #pragma unroll
-      for (int m = 0; m < MT; ++m) load(av, asv, j.a, 16 * m + r16, kb, a[m], sa[m]);
+      for (int m = 0; m < MT; ++m) {
+        const v4i w = *reinterpret_cast<const v4i*>(pa + (16 * m + r16) * 128 + at);
+        a[m] = v8i{w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+        sa[m] = psa[(h * TM + 16 * m + r16) * 4 + q];
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
           acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[n], a[m], acc[m][n], 4, 4, 0, sb[n], 0, sa[m]);
     }
+    // the slot's reads are done (the MFMAs have their operands): refill it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    issue(i + D);
   }
+  wait_loads<0>();
+  __syncthreads();
+  float(*part)[TM][PITCH] = reinterpret_cast<float(*)[TM][PITCH]>(smem);
   // every path out of the loop waits the last MFMAs out before the accumulators are read
   __builtin_amdgcn_sched_barrier(0);
   mfma_drain();
@@ -118,8 +185,6 @@ constexpr int F4_ROWB = F4_KSTEP / 2;
 constexpr int F4_DATA = BM2 * F4_ROWB;              // per operand and stage
 constexpr int F4_SC = BM2 * 8;                       // scale bytes per operand and stage: [K slice][row] dwords
 constexpr int F4_STAGE = 2 * (F4_DATA + F4_SC);      // A data, B data, A scales, B scales
-
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 // acc += B . A^T for one 64-wide substep; the scale of each operand is byte KK of its dword
 template <int KK>
