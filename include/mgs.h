@@ -378,7 +378,7 @@ int mgs_moe_route_bwd(const mgs_route_params* params, int64_t tokens, int32_t ex
                       const void* logits, int32_t logits_dtype, int64_t ld, const int32_t* expert_idx,
                       const float* dweights, void* dlogits, int64_t ld_dlogits, void* stream);
 
-/* Workspace bytes of mgs_moe_dispatch.  Negative MGS_ERR_* on invalid arguments. */
+/* Workspace bytes of mgs_moe_dispatch (0 for few slots).  Negative MGS_ERR_* on invalid arguments. */
 int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t experts);
 
 /* Tokens into expert order: a stable sort of the slots by expert, and the token rows copied to it.
@@ -390,8 +390,9 @@ int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t e
  *                rows past the last used one are left as they were
  *   weights, row_weights  both or neither: row_weights[row_of_slot[s]] = weights[s] ([tokens x topk], the
  *                per-row scale `probs` of the activation calls)
- *   workspace    mgs_moe_dispatch_workspace_bytes() bytes of scratch, caller-owned, contents undefined
- *                before and after; calls sharing it must not overlap */
+ *   workspace    mgs_moe_dispatch_workspace_bytes() bytes of scratch (ignored, may be NULL, when that
+ *                is 0), caller-owned, contents undefined before and after; calls sharing it must not
+ *                overlap */
 int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_t* expert_idx, int64_t hidden,
                      int32_t dtype, const void* x, int64_t ldx, const float* weights, void* rows,
                      int64_t num_rows, float* row_weights, int32_t* row_of_slot, int64_t* split_sizes,

@@ -41,7 +41,7 @@ class ActParams(ctypes.Structure):
 
 
 class Groups(ctypes.Structure):
-    _fields_ = [("num_groups", ctypes.c_int32), ("split_sizes", ctypes.POINTER(ctypes.c_int64)),
+    _fields_ = [("num_groups", ctypes.c_int32), ("split_sizes", ctypes.c_void_p),
                 ("max_rows", ctypes.c_int64), ("dev_table", ctypes.c_void_p)]
 
 
@@ -149,17 +149,19 @@ class DeviceGroups:
 class _GroupsArg:
     """Keeps the int64 split array alive for the duration of a call."""
 
+    __slots__ = ("arr", "struct", "ref")
+
     def __init__(self, split_sizes):
         if isinstance(split_sizes, DeviceGroups):
             self.arr = None
             self.struct = Groups(split_sizes.num_groups, None, split_sizes.max_rows, split_sizes.table.data_ptr())
-            return
-        self.arr = np.ascontiguousarray(np.asarray(split_sizes, dtype=np.int64))
-        self.struct = Groups(len(self.arr), self.arr.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), 0, None)
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.struct)
+        elif type(split_sizes) is list and all(type(m) is int for m in split_sizes):
+            self.arr = (ctypes.c_int64 * len(split_sizes))(*split_sizes)
+            self.struct = Groups(len(split_sizes), ctypes.addressof(self.arr), 0, None)
+        else:
+            self.arr = np.ascontiguousarray(np.asarray(split_sizes, dtype=np.int64))
+            self.struct = Groups(len(self.arr), self.arr.ctypes.data, 0, None)
+        self.ref = ctypes.byref(self.struct)
 
 
 def _ptr(t):
@@ -173,7 +175,7 @@ def _ptr(t):
 def _stream(stream):
     """HIP stream handle: an int passes through (0 = null stream), None = torch's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -190,11 +192,12 @@ class QTensor:
         """`rht` (NVFP4 columnwise only): 16-bit sign mask of the Hadamard transform of the copy."""
         self.fmt, self.colwise, self.width = fmt, bool(colwise), int(width)
         self.rht = 0 if rht is None else RHT_ON | (int(rht) & 0xFFFF)
-        nd = qtensor_nbytes(fmt, colwise, split_sizes, width, "data")
-        ns = qtensor_nbytes(fmt, colwise, split_sizes, width, "scales")
-        ng = qtensor_nbytes(fmt, colwise, split_sizes, width, "group_scale")
-        self.data = torch.empty(max(nd, 1), dtype=torch.uint8, device=device)[:nd]
-        self.scales = torch.empty(max(ns, 1), dtype=torch.uint8, device=device)[:ns]
+        g, f = _GroupsArg(split_sizes), FMT[fmt]
+        nd, ns, ng = (LIB.mgs_qtensor_nbytes(f, int(self.colwise), g.ref, self.width, w) for w in (0, 1, 2))
+        if min(nd, ns, ng) < 0:
+            _check(int(min(nd, ns, ng)))
+        self.data = torch.empty(nd, dtype=torch.uint8, device=device) if nd else torch.empty(1, dtype=torch.uint8, device=device)[:0]
+        self.scales = torch.empty(ns, dtype=torch.uint8, device=device) if ns else torch.empty(1, dtype=torch.uint8, device=device)[:0]
         self.group_scale = torch.empty(ng // 4, dtype=torch.float32, device=device) if ng else None
 
     def qbuf(self):

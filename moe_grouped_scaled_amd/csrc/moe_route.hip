@@ -19,9 +19,13 @@ namespace {
 // ------------------------------------------------------------------------------------------ router
 //
 // Sixteen lanes (one DPP row) own a token, four tokens a wave; lane l holds the logits of experts
-// l, l + 16, ... as integer keys that order like the values.  A pick is a maximum over the lane's keys and
-// four DPP steps, then the lowest expert that holds it the same way.
-
+// l, l + 16, ... as 32-bit keys that order like the values, the last byte of a key replaced by 255 - expert,
+// so that keys are unique and equal values order by expert.  A pick is a maximum over the lane's keys and
+// four DPP steps; the next one is the largest key below it: with unsigned wrap-around, key - M is larger
+// the closer the key lies below M, and small for the keys already taken, so M + max(key - M) is the next
+// pick and nothing has to be marked as taken.  Replacing the last byte is exact for BF16 logits (and FP32
+// ones whose last byte is zero); for others a wave in which two neighbouring picks, or the last pick and
+// the next key, agree in the other 24 bits picks again with whole keys.
 constexpr int ROUTE_LANES = 16;
 constexpr int DPP_ROW_ROR1 = 0x121, DPP_ROW_ROR2 = 0x122;
 
@@ -65,22 +69,15 @@ struct RouteArgs {
   int64_t ld, ldd;
 };
 
-template <typename T, int EPL>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __restrict__ logits,
-                                                    int32_t* __restrict__ idx, float* __restrict__ weights) {
-  const int l = threadIdx.x & (ROUTE_LANES - 1);
-  const int64_t t = (int64_t)blockIdx.x * (256 / ROUTE_LANES) + (threadIdx.x >> 4);
-  const bool there = t < a.tokens;
+// The topk picks of a token by whole keys: lane c < topk gets choice c (-1: none).  Two reductions and a
+// pass that clears the pick, each round.
+template <int EPL>
+__device__ __forceinline__ int pick_exact(const float (&x)[EPL], int experts, int topk, int l) {
   uint32_t key[EPL];
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    const int e = ROUTE_LANES * j + l;
-    key[j] = there && e < a.experts ? logit_key(load_logit(logits + t * a.ld + e)) : 0u;
-  }
-  const bool full_sum = a.score == MGS_SCORE_SOFTMAX && !a.renormalize;
-  float top = 0.0f, sum = 0.0f, mine = 0.0f;  // lane c keeps choice c's score
+  for (int j = 0; j < EPL; ++j) key[j] = ROUTE_LANES * j + l < experts ? logit_key(x[j]) : 0u;
   int pick = -1;
-  for (int c = 0; c < a.topk; ++c) {
+  for (int c = 0; c < topk; ++c) {
     uint32_t m = key[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) m = umax(m, key[j]);
@@ -90,32 +87,72 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __rest
     for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? ROUTE_LANES * j + l : at;
     // lowest expert among the lanes that hold m, as a maximum of the complement
     const int e = (int)~row_umax(at < 0 ? 0u : ~(uint32_t)at);
-    const bool ok = m > KEY_NEG_INF;
-    const float x = key_logit(m);
-    if (c == 0) {
-      top = ok ? x : 0.0f;
-      if (full_sum) {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) s += key[j] > KEY_NEG_INF ? expf(key_logit(key[j]) - top) : 0.0f;
-        sum = row_sum(s);
-      }
-    }
-    float p = 0.0f;
-    if (ok) p = a.score == MGS_SCORE_SOFTMAX ? expf(x - top) : 1.0f / (1.0f + expf(-x));
-    if (!full_sum && a.renormalize) sum += p;
-    if (l == c) {
-      mine = p;
-      pick = ok ? e : -1;
-    }
+    if (l == c) pick = m > KEY_NEG_INF ? e : -1;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) key[j] = ROUTE_LANES * j + l == e ? 0u : key[j];
   }
+  return pick;
+}
+
+template <typename T, int EPL>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __restrict__ logits,
+                                                    int32_t* __restrict__ idx, float* __restrict__ weights) {
+  const int l = threadIdx.x & (ROUTE_LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (256 / ROUTE_LANES) + (threadIdx.x >> 4);
+  const bool there = t < a.tokens;
+  const T* row = logits + (there ? t : 0) * a.ld;
+  float x[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = ROUTE_LANES * j + l;
+    x[j] = there && e < a.experts ? load_logit(row + e) : -INFINITY;
+  }
+  uint32_t key[EPL], low = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = ROUTE_LANES * j + l;
+    low |= __float_as_uint(x[j]);
+    key[j] = e < a.experts ? (logit_key(x[j]) & ~0xffu) | (uint32_t)(255 - e) : 0u;
+  }
+  // experts at or below this key are not available (-inf with any last byte)
+  constexpr uint32_t NONE = KEY_NEG_INF | 0xffu;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) m = umax(m, key[j]);
+  m = row_umax(m);
+  int pick = -1;
+  bool again = false;
+  for (int c = 0; c < a.topk; ++c) {
+    if (l == c && m > NONE) pick = 255 - (int)(m & 0xffu);
+    uint32_t d = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) d = umax(d, key[j] - m);
+    const uint32_t next = m + row_umax(d);
+    // next >= m: nothing is left below m
+    again |= next < m && next > NONE && ((next ^ m) >> 8) == 0u;
+    m = next < m ? next : 0u;
+  }
+  if (sizeof(T) == 4 && __ballot(again) != 0 && __ballot((low & 0xffu) != 0) != 0) pick = pick_exact<EPL>(x, a.experts, a.topk, l);
+  const float v = there && pick >= 0 ? load_logit(row + pick) : 0.0f;
+  float p = 0.0f, sum = 0.0f;
+  const bool full_sum = a.score == MGS_SCORE_SOFTMAX && !a.renormalize;
+  if (a.score == MGS_SCORE_SOFTMAX) {
+    const float top = __shfl(v, 0, ROUTE_LANES);  // the first pick is the maximum
+    if (pick >= 0) p = expf(v - top);
+    if (full_sum) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) sum += x[j] == -INFINITY ? 0.0f : expf(x[j] - top);
+      sum = row_sum(sum);
+    }
+  } else if (pick >= 0) {
+    p = 1.0f / (1.0f + expf(-v));
+  }
+  if (a.renormalize) sum = row_sum(p);
   if (there && l < a.topk) {
     idx[t * a.topk + l] = pick;
-    float w = mine;
+    float w = p;
     // a sum of 0 (sigmoid scores that all underflow) leaves the weights 0
-    if (pick >= 0 && (full_sum || a.renormalize) && sum != 0.0f) w = mine / sum;
+    if (pick >= 0 && (full_sum || a.renormalize) && sum != 0.0f) w = p / sum;
     weights[t * a.topk + l] = w * a.scale;
   }
 }
@@ -128,9 +165,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
                                                         const int32_t* __restrict__ idx,
                                                         const float* __restrict__ dweights,
                                                         T* __restrict__ dlogits) {
+  // the token's gradients, laid out by expert, and one slot for choices without one
+  __shared__ float out_lds[256 / ROUTE_LANES][ROUTE_LANES * EPL + 1];
   const int l = threadIdx.x & (ROUTE_LANES - 1);
   const int64_t t = (int64_t)blockIdx.x * (256 / ROUTE_LANES) + (threadIdx.x >> 4);
   const bool there = t < a.tokens;
+  float* line = out_lds[threadIdx.x >> 4];
   int e = -1;
   float g = 0.0f, x = 0.0f;
   if (there && l < a.topk) {
@@ -147,19 +187,24 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
   float rest = 0.0f;         // softmax weight of the experts that were not picked
   if (softmax) {
     // maximum and sum over the picked experts, or over all of them
-    float top = row_umax(e >= 0 ? logit_key(x) : 0u) > KEY_NEG_INF ? key_logit(row_umax(e >= 0 ? logit_key(x) : 0u)) : 0.0f;
+    const uint32_t best = row_umax(e >= 0 ? logit_key(x) : 0u);
+    const float top = best > KEY_NEG_INF ? key_logit(best) : 0.0f;
     float sum;
     p = e >= 0 ? expf(x - top) : 0.0f;
     if (dense) {
+      // the picked experts are marked so that the others' sum can be taken on its own
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) line[ROUTE_LANES * j + l] = 0.0f;
+      __builtin_amdgcn_wave_barrier();
+      line[e >= 0 ? e : ROUTE_LANES * EPL] = 1.0f;
+      __builtin_amdgcn_wave_barrier();
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
         const int at = ROUTE_LANES * j + l;
-        float v = there && at < a.experts ? load_logit(logits + t * a.ld + at) : 0.0f;
-        ex[j] = there && at < a.experts ? expf(v - top) : 0.0f;
-        bool picked = false;
-        for (int i = 0; i < a.topk; ++i) picked |= __shfl(e, i, ROUTE_LANES) == at;
-        s += picked ? 0.0f : ex[j];
+        const bool in = there && at < a.experts;
+        ex[j] = in ? expf(load_logit(logits + t * a.ld + at) - top) : 0.0f;
+        s += line[at] != 0.0f ? 0.0f : ex[j];
       }
       rest = row_sum(s);
       sum = rest + row_sum(p);
@@ -194,19 +239,16 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
     d = g * p * q;
   }
   const float others = dense ? -row_sum(w * g) : 0.0f;  // of the experts not picked: -p_e sum_i w_i g_i
-  float out[EPL];
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) out[j] = dense ? ex[j] * others : 0.0f;
-  for (int i = 0; i < a.topk; ++i) {
-    const int ei = __shfl(e, i, ROUTE_LANES);
-    const float di = __shfl(d, i, ROUTE_LANES);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) out[j] = ei == ROUTE_LANES * j + l ? di : out[j];
-  }
+  for (int j = 0; j < EPL; ++j) line[ROUTE_LANES * j + l] = dense ? ex[j] * others : 0.0f;
+  __builtin_amdgcn_wave_barrier();
+  line[e >= 0 ? e : ROUTE_LANES * EPL] = d;
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int at = ROUTE_LANES * j + l;
-    if (there && at < a.experts) store_value(dlogits + t * a.ldd + at, out[j]);
+    if (there && at < a.experts) store_value(dlogits + t * a.ldd + at, line[at]);
   }
 }
 
@@ -220,50 +262,65 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
 // blocks before it stays short.
 __host__ __device__ inline int sort_chunk(int64_t slots) { return slots <= 131072 ? 1024 : 4096; }
 
+// Up to this many slots the dispatch is one launch whose workgroups each look at all of them.
+constexpr int64_t SMALL_SLOTS = 2048;
+
 __device__ __forceinline__ int slot_expert(const int32_t* __restrict__ idx, int64_t s, int64_t slots, int experts) {
   const int e = s < slots ? idx[s] : -1;
   return e >= 0 && e < experts ? e : -1;
 }
 
-__global__ __launch_bounds__(256) void sort_count_kernel(int64_t slots, int experts, int chunk,
-                                                         const int32_t* __restrict__ idx, int32_t* __restrict__ counts) {
+template <int CHUNK>
+__global__ __launch_bounds__(256) void sort_count_kernel(int64_t slots, int experts, const int32_t* __restrict__ idx,
+                                                         int32_t* __restrict__ counts) {
   __shared__ int32_t h[MGS_MAX_GROUPS];
   h[threadIdx.x] = 0;
+  const int64_t s0 = (int64_t)blockIdx.x * CHUNK;
+  int e[CHUNK / 256];
+#pragma unroll
+  for (int i = 0; i < CHUNK / 256; ++i) e[i] = slot_expert(idx, s0 + 256 * i + threadIdx.x, slots, experts);
   __syncthreads();
-  const int64_t s0 = (int64_t)blockIdx.x * chunk;
-  for (int i = threadIdx.x; i < chunk; i += 256) {
-    const int e = slot_expert(idx, s0 + i, slots, experts);
-    if (e >= 0) atomicAdd(&h[e], 1);
-  }
+#pragma unroll
+  for (int i = 0; i < CHUNK / 256; ++i)
+    if (e[i] >= 0) atomicAdd(&h[e[i]], 1);
   __syncthreads();
   if ((int)threadIdx.x < experts) counts[(int64_t)blockIdx.x * experts + threadIdx.x] = h[threadIdx.x];
 }
 
 // Exclusive sum over the 256 threads of a workgroup.
 __device__ __forceinline__ int block_exclusive(int v, int32_t* lds) {
-  const int t = threadIdx.x;
-  lds[t] = v;
-  __syncthreads();
-  for (int d = 1; d < 256; d <<= 1) {
-    const int o = t >= d ? lds[t - d] : 0;
-    __syncthreads();
-    lds[t] += o;
-    __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d);
+    s += lane >= d ? o : 0;
   }
-  return lds[t] - v;
+  if (lane == 63) lds[wave] = s;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 3; ++w) s += w < wave ? lds[w] : 0;
+  return s - v;
 }
 
-__global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int experts, int chunk,
-                                                        const int32_t* __restrict__ idx,
+template <int CHUNK>
+__global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int experts, const int32_t* __restrict__ idx,
                                                         const int32_t* __restrict__ counts,
                                                         int32_t* __restrict__ row_of_slot,
                                                         int64_t* __restrict__ splits) {
-  __shared__ int32_t scan[256];
+  __shared__ int32_t scan[4];
   __shared__ int32_t next[4][MGS_MAX_GROUPS];  // the next row of each expert, per wave
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  // wave w owns the w-th quarter of the chunk; its rows follow those of the waves before it
+  constexpr int PER = CHUNK / 4;
+  const int64_t s0 = (int64_t)blockIdx.x * CHUNK + (int64_t)wave * PER;
+  int e[PER / 64];
+#pragma unroll
+  for (int i = 0; i < PER / 64; ++i) e[i] = slot_expert(idx, s0 + 64 * i + lane, slots, experts);
   int before = 0, total = 0;
   if (t < experts) {
     const int nb = gridDim.x;
+#pragma unroll 8
     for (int b = 0; b < nb; ++b) {
       const int v = counts[(int64_t)b * experts + t];
       before += b < (int)blockIdx.x ? v : 0;
@@ -271,19 +328,13 @@ __global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int exper
     }
     if (blockIdx.x == 0) splits[t] = total;
   }
-  const int base = block_exclusive(total, scan) + before;
 #pragma unroll
   for (int w = 0; w < 4; ++w) next[w][t] = 0;
+  int r = block_exclusive(total, scan) + before;  // (its barrier also stands between the zeros and the counts)
+#pragma unroll
+  for (int i = 0; i < PER / 64; ++i)
+    if (e[i] >= 0) atomicAdd(&next[wave][e[i]], 1);
   __syncthreads();
-  // wave w owns the w-th quarter of the chunk; its rows follow those of the waves before it
-  const int per = chunk / 4;
-  const int64_t s0 = (int64_t)blockIdx.x * chunk + (int64_t)wave * per;
-  for (int i = lane; i < per; i += 64) {
-    const int e = slot_expert(idx, s0 + i, slots, experts);
-    if (e >= 0) atomicAdd(&next[wave][e], 1);
-  }
-  __syncthreads();
-  int r = base;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const int c = next[w][t];
@@ -291,21 +342,21 @@ __global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int exper
     r += c;
   }
   __syncthreads();
-  for (int i = lane; i < per; i += 64) {
-    const int64_t s = s0 + i;
-    const int e = slot_expert(idx, s, slots, experts);
+#pragma unroll
+  for (int i = 0; i < PER / 64; ++i) {
+    const int64_t s = s0 + 64 * i + lane;
     // lanes with the same expert: one ballot per bit of it
-    uint64_t same = __ballot(e >= 0);
+    uint64_t same = __ballot(e[i] >= 0);
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
-      const uint64_t v = __ballot((e >> b) & 1);
-      same &= (e >> b) & 1 ? v : ~v;
+      const uint64_t v = __ballot((e[i] >> b) & 1);
+      same &= (e[i] >> b) & 1 ? v : ~v;
     }
     const int rank = __popcll(same & ((1ull << lane) - 1));
     int row = -1;
-    if (e >= 0) row = next[wave][e] + rank;
+    if (e[i] >= 0) row = next[wave][e[i]] + rank;
     __builtin_amdgcn_wave_barrier();
-    if (e >= 0 && rank == 0) next[wave][e] += __popcll(same);
+    if (e[i] >= 0 && rank == 0) next[wave][e[i]] += __popcll(same);
     __builtin_amdgcn_wave_barrier();
     if (s < slots) row_of_slot[s] = row;
   }
@@ -316,16 +367,28 @@ __global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int exper
 // Rows are moved in units of V elements (16 bytes where widths, strides and addresses allow it, else
 // single elements).  A token's units are spread over `tpt` threads, a power of two up to 256.
 
+// the same bits, unconverted
+template <typename T, int V>
+struct Raw { typedef uint4 type; };
+template <>
+struct Raw<float, 1> { typedef float type; };
+template <>
+struct Raw<uint16_t, 1> { typedef uint16_t type; };
+
+template <typename T, int V>
+__device__ __forceinline__ void unit_unpack(const typename Raw<T, V>::type& w, float (&v)[V]) {
+  if constexpr (V == 8) {
+    unpack8(w, v);
+  } else if constexpr (V == 4) {
+    v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+  } else {
+    v[0] = load_logit(&w);
+  }
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void unit_load(const T* p, float (&v)[V]) {
-  if constexpr (V == 8) {
-    unpack8(*reinterpret_cast<const uint4*>(p), v);
-  } else if constexpr (V == 4) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-  } else {
-    v[0] = load_logit(p);
-  }
+  unit_unpack<T, V>(*reinterpret_cast<const typename Raw<T, V>::type*>(p), v);
 }
 
 // The data registers of a 16-byte store stay live through two wait states after it (a VALU write to one of
@@ -348,13 +411,6 @@ __device__ __forceinline__ void unit_store(T* p, const float (&v)[V]) {
   }
 }
 
-// the same bits, unconverted
-template <typename T, int V>
-struct Raw { typedef uint4 type; };
-template <>
-struct Raw<float, 1> { typedef float type; };
-template <>
-struct Raw<uint16_t, 1> { typedef uint16_t type; };
 __device__ __forceinline__ void raw_store(uint4* p, uint4 v) { store16(p, v); }
 __device__ __forceinline__ void raw_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void raw_store(uint16_t* p, uint16_t v) { *p = v; }
@@ -372,101 +428,202 @@ __device__ __forceinline__ int slot_row(const MoveArgs& a, const int32_t* __rest
   return r >= 0 && r < a.num_rows ? r : -1;
 }
 
-// x row of every token into the rows of its slots
-template <typename T, int V>
+// x row of every token into the rows of its slots (the token's unit is read once)
+template <typename T, int V, int KMAX>
+__device__ __forceinline__ void scatter_row(const MoveArgs& a, const int (&r)[KMAX], const T* __restrict__ x,
+                                            T* __restrict__ rows, int u, int tpt) {
+  typedef typename Raw<T, V>::type R;
+  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V * tpt) {
+    const R v = *reinterpret_cast<const R*>(x + h);
+#pragma unroll
+    for (int c = 0; c < KMAX; ++c)
+      if (c < a.topk && r[c] >= 0) raw_store(reinterpret_cast<R*>(rows + (int64_t)r[c] * a.hidden + h), v);
+  }
+}
+
+template <typename T, int V, int KMAX>
 __global__ __launch_bounds__(256) void scatter_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
                                                       const T* __restrict__ x, const float* __restrict__ weights,
                                                       T* __restrict__ rows, float* __restrict__ row_weights) {
-  typedef typename Raw<T, V>::type R;
-  const int u = threadIdx.x & ((1 << a.tpt_log2) - 1);
+  const int tpt = 1 << a.tpt_log2, u = threadIdx.x & (tpt - 1);
   const int64_t t = ((int64_t)blockIdx.x << (8 - a.tpt_log2)) + (threadIdx.x >> a.tpt_log2);
   if (t >= a.tokens) return;
-  if (row_weights && u < a.topk) {
-    for (int c = u; c < a.topk; c += 1 << a.tpt_log2) {
+  if (row_weights) {
+    for (int c = u; c < a.topk; c += tpt) {
       const int r = slot_row(a, row_of_slot, t, c);
       if (r >= 0) row_weights[r] = weights[t * a.topk + c];
     }
   }
-  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V << a.tpt_log2) {
-    const R v = *reinterpret_cast<const R*>(x + t * a.ld + h);
-    for (int c = 0; c < a.topk; ++c) {
-      const int r = slot_row(a, row_of_slot, t, c);
-      if (r >= 0) raw_store(reinterpret_cast<R*>(rows + (int64_t)r * a.hidden + h), v);
-    }
-  }
+  int r[KMAX];
+#pragma unroll
+  for (int c = 0; c < KMAX; ++c) r[c] = c < a.topk ? slot_row(a, row_of_slot, t, c) : -1;
+  scatter_row<T, V, KMAX>(a, r, x + t * a.ld, rows, u, tpt);
 }
 
-// y of every token: the sum over its slots' rows in slot order, in FP32, with weights if given
-template <typename T, int V>
+// The whole dispatch in one launch, for few slots: a workgroup per token counts, over all slots, those that
+// precede each of its own in the sorted order, then copies its row.  Workgroup 0 also takes the split sizes.
+template <typename T, int V, int KMAX>
+__global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slots, const int32_t* __restrict__ idx,
+                                                             const T* __restrict__ x, const float* __restrict__ weights,
+                                                             T* __restrict__ rows, float* __restrict__ row_weights,
+                                                             int32_t* __restrict__ row_of_slot,
+                                                             int64_t* __restrict__ splits) {
+  __shared__ int32_t part[4][KMAX];
+  __shared__ int32_t hist[MGS_MAX_GROUPS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t t = blockIdx.x;
+  const int slot0 = (int)t * a.topk;
+  int mine[KMAX], n[KMAX];
+#pragma unroll
+  for (int c = 0; c < KMAX; ++c) {
+    n[c] = 0;
+    mine[c] = c < a.topk && t < a.tokens ? slot_expert(idx, slot0 + c, slots, a.experts) : -1;
+  }
+  hist[tid] = 0;
+  __syncthreads();
+  for (int s0 = 64 * wave; s0 < slots; s0 += 256) {
+    const int s = s0 + lane;
+    const int e = slot_expert(idx, s, slots, a.experts);
+    if (blockIdx.x == 0 && e >= 0) atomicAdd(&hist[e], 1);
+#pragma unroll
+    for (int c = 0; c < KMAX; ++c)
+      if (c < a.topk) n[c] += __popcll(__ballot(e >= 0 && (e < mine[c] || (e == mine[c] && s < slot0 + c))));
+  }
+#pragma unroll
+  for (int c = 0; c < KMAX; ++c)
+    if (lane == c) part[wave][c] = n[c];
+  __syncthreads();
+  if (blockIdx.x == 0 && tid < a.experts) splits[tid] = hist[tid];
+  if (t >= a.tokens) return;
+  int r[KMAX];
+#pragma unroll
+  for (int c = 0; c < KMAX; ++c) {
+    r[c] = mine[c] >= 0 ? part[0][c] + part[1][c] + part[2][c] + part[3][c] : -1;
+    if (tid == c && c < a.topk) {
+      row_of_slot[slot0 + c] = r[c];
+      if (row_weights && r[c] >= 0) row_weights[r[c]] = weights[slot0 + c];
+    }
+  }
+  if (rows) scatter_row<T, V, KMAX>(a, r, x + t * a.ld, rows, tid, 256);
+}
+
+// y of every token: the sum over its slots' rows in slot order, in FP32, with weights if given.  Row numbers
+// and weights are read once; the loads of eight rows go out before their sums.
+template <typename T, int V, int KMAX>
 __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
                                                       const T* __restrict__ rows, const float* __restrict__ weights,
                                                       T* __restrict__ y, const float* __restrict__ drow_weights,
                                                       float* __restrict__ dweights) {
-  const int u = threadIdx.x & ((1 << a.tpt_log2) - 1);
+  typedef typename Raw<T, V>::type R;
+  constexpr int GROUP = KMAX < 8 ? KMAX : 8;
+  const int tpt = 1 << a.tpt_log2, u = threadIdx.x & (tpt - 1);
   const int64_t t = ((int64_t)blockIdx.x << (8 - a.tpt_log2)) + (threadIdx.x >> a.tpt_log2);
   if (t >= a.tokens) return;
   if (dweights) {
-    for (int c = u; c < a.topk; c += 1 << a.tpt_log2) {
+    for (int c = u; c < a.topk; c += tpt) {
       const int r = slot_row(a, row_of_slot, t, c);
       dweights[t * a.topk + c] = r >= 0 ? drow_weights[r] : 0.0f;
     }
   }
-  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V << a.tpt_log2) {
+  int r[KMAX];
+  float w[KMAX];
+#pragma unroll
+  for (int c = 0; c < KMAX; ++c) {
+    r[c] = c < a.topk ? slot_row(a, row_of_slot, t, c) : -1;
+    w[c] = weights && r[c] >= 0 ? weights[t * a.topk + c] : 1.0f;
+  }
+  for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V * tpt) {
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    for (int c = 0; c < a.topk; ++c) {
-      const int r = slot_row(a, row_of_slot, t, c);
-      if (r < 0) continue;
-      float v[V];
-      unit_load<T, V>(rows + (int64_t)r * a.hidden + h, v);
-      const float w = weights ? weights[t * a.topk + c] : 1.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+    for (int c0 = 0; c0 < KMAX; c0 += GROUP) {
+      if (c0 >= a.topk) break;
+      R v[GROUP];
+#pragma unroll
+      for (int c = 0; c < GROUP; ++c)
+        if (r[c0 + c] >= 0) v[c] = *reinterpret_cast<const R*>(rows + (int64_t)r[c0 + c] * a.hidden + h);
+#pragma unroll
+      for (int c = 0; c < GROUP; ++c) {
+        if (r[c0 + c] < 0) continue;
+        float f[V];
+        unit_unpack<T, V>(v[c], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(w[c0 + c], f[i], acc[i]);
+      }
     }
     unit_store<T, V>(y + t * a.ld + h, acc);
   }
 }
 
-// d(rows) = w dy and d(w) = <dy, rows> of every slot; one workgroup per token
+// d(rows) = w dy and d(w) = <dy, rows>, four slots of a token at a time: a unit of dy is read once for them.
+// The sums run over the token's threads by lane exchanges, then over its waves in order.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
                                                           const T* __restrict__ dy, const T* __restrict__ rows,
                                                           const float* __restrict__ weights, T* __restrict__ drows,
                                                           float* __restrict__ dweights) {
-  __shared__ float part[4];
-  const int64_t t = blockIdx.x;
-  for (int c = 0; c < a.topk; ++c) {
-    const int r = slot_row(a, row_of_slot, t, c);
-    if (r < 0) {
-      if (dweights && threadIdx.x == 0) dweights[t * a.topk + c] = 0.0f;
-      continue;
-    }
-    const float w = weights ? weights[t * a.topk + c] : 1.0f;
-    float dot = 0.0f;
-    for (int64_t h = (int64_t)threadIdx.x * V; h < a.hidden; h += (int64_t)V * 256) {
-      float g[V];
-      unit_load<T, V>(dy + t * a.ld + h, g);
-      if (dweights) {
-        float v[V];
-        unit_load<T, V>(rows + (int64_t)r * a.hidden + h, v);
+  __shared__ float part[4][4];
+  const int tpt = 1 << a.tpt_log2, u = threadIdx.x & (tpt - 1);
+  const int64_t t = ((int64_t)blockIdx.x << (8 - a.tpt_log2)) + (threadIdx.x >> a.tpt_log2);
+  const bool there = t < a.tokens;
+  const int width = tpt < 64 ? tpt : 64;
+  for (int c0 = 0; c0 < a.topk; c0 += 4) {
+    int r[4];
+    float w[4], dot[4];
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot = __builtin_fmaf(g[i], v[i], dot);
-      }
-      if (drows) {
-        float o[V];
+    for (int c = 0; c < 4; ++c) {
+      r[c] = there && c0 + c < a.topk ? slot_row(a, row_of_slot, t, c0 + c) : -1;
+      w[c] = r[c] >= 0 && weights ? weights[t * a.topk + c0 + c] : 1.0f;
+      dot[c] = 0.0f;
+    }
+    if (there) {
+      for (int64_t h = (int64_t)u * V; h < a.hidden; h += (int64_t)V * tpt) {
+        float g[V];
+        unit_load<T, V>(dy + t * a.ld + h, g);
+        if (dweights) {
+          float v[4][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = w * g[i];
-        unit_store<T, V>(drows + (int64_t)r * a.hidden + h, o);
+          for (int c = 0; c < 4; ++c)
+            if (r[c] >= 0) unit_load<T, V>(rows + (int64_t)r[c] * a.hidden + h, v[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (r[c] >= 0) {
+#pragma unroll
+              for (int i = 0; i < V; ++i) dot[c] = __builtin_fmaf(g[i], v[c][i], dot[c]);
+            }
+        }
+        if (drows) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = w[c] * g[i];
+            if (r[c] >= 0) unit_store<T, V>(drows + (int64_t)r[c] * a.hidden + h, o);
+          }
+        }
       }
     }
-    if (dweights) {
-      for (int d = 32; d; d >>= 1) dot += __shfl_xor(dot, d);
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+    if (!dweights) continue;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      for (int d = width >> 1; d; d >>= 1) dot[c] += __shfl_xor(dot[c], d);
+    if (tpt > 64) {
       __syncthreads();
-      if (threadIdx.x == 0) dweights[t * a.topk + c] = ((part[0] + part[1]) + part[2]) + part[3];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][c] = dot[c];
       __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int w0 = (threadIdx.x >> a.tpt_log2) << (a.tpt_log2 - 6);  // the token's first wave
+        dot[c] = part[w0][c] + part[w0 + 1][c];
+        if (tpt == 256) dot[c] += part[2][c] + part[3][c];
+      }
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (there && u == 0 && c0 + c < a.topk) dweights[t * a.topk + c0 + c] = r[c] >= 0 ? dot[c] : 0.0f;
   }
 }
 
@@ -484,6 +641,16 @@ void with_unit(int dtype, bool wide, F f) {
     if (wide) f(float{}, std::integral_constant<int, 4>{});
     else f(float{}, std::integral_constant<int, 1>{});
   }
+}
+
+// calls f(bound of topk): per-slot registers are sized by it (two slots in arrays of sixteen cost the combine
+// of 16384 tokens x 4096 108 instead of 92 us)
+template <typename F>
+void with_topk(int topk, F f) {
+  if (topk <= 2) f(std::integral_constant<int, 2>{});
+  else if (topk <= 4) f(std::integral_constant<int, 4>{});
+  else if (topk <= 8) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
 }
 
 // 16-byte units need whole units per row, aligned rows and aligned tensors
@@ -599,6 +766,7 @@ int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t e
   if (tokens < 0 || tokens > INT32_MAX / topk) return fail(MGS_ERR_SHAPE, "tokens %lld: tokens x topk must be in [0, 2^31)", (long long)tokens);
   const int64_t slots = tokens * topk, chunk = sort_chunk(slots);
   ok();
+  if (slots <= SMALL_SLOTS) return 0;
   return 4 * std::max<int64_t>(1, (slots + chunk - 1) / chunk) * experts;
 }
 
@@ -622,23 +790,44 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
   if (!expert_idx && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "expert_idx is NULL");
   if (!row_of_slot && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot is NULL");
   if (!split_sizes) return fail(MGS_ERR_INVALID_ARG, "split_sizes is NULL");
-  if (!workspace || workspace_bytes < need)
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(MGS_ERR_INVALID_ARG, "the sort needs a workspace of %lld bytes (got %lld%s)", (long long)need,
                 (long long)workspace_bytes, workspace ? "" : ", NULL");
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  const int chunk = sort_chunk(slots);
-  const dim3 grid((unsigned)std::max<int64_t>(1, (slots + chunk - 1) / chunk));
+  const bool wide = x && wide_rows(dtype, hidden, ldx, {x, rows});
+  a.experts = experts;
+  a.topk = topk;
+  a.tokens = tokens;
+  if (slots <= SMALL_SLOTS) {
+    with_unit(dtype, wide, [&](auto e, auto n) {
+      typedef decltype(e) T;
+      with_topk(topk, [&](auto k) {
+        hipLaunchKernelGGL((dispatch_small_kernel<T, decltype(n)::value, decltype(k)::value>), dim3((unsigned)std::max<int64_t>(1, tokens)),
+                           dim3(256), 0, st, a, (int)slots, expert_idx, static_cast<const T*>(x), weights,
+                           static_cast<T*>(tokens ? rows : nullptr), row_weights, row_of_slot, split_sizes);
+      });
+    });
+    return launched();
+  }
   int32_t* counts = static_cast<int32_t*>(workspace);
-  hipLaunchKernelGGL(sort_count_kernel, grid, dim3(256), 0, st, slots, experts, chunk, expert_idx, counts);
-  hipLaunchKernelGGL(sort_rows_kernel, grid, dim3(256), 0, st, slots, experts, chunk, expert_idx, counts, row_of_slot, split_sizes);
-  if (x && tokens > 0) {
-    with_unit(dtype, wide_rows(dtype, hidden, ldx, {x, rows}), [&](auto e, auto n) {
+  auto sort = [&](auto c) {
+    constexpr int CHUNK = decltype(c)::value;
+    const dim3 grid((unsigned)((slots + CHUNK - 1) / CHUNK));
+    hipLaunchKernelGGL(sort_count_kernel<CHUNK>, grid, dim3(256), 0, st, slots, experts, expert_idx, counts);
+    hipLaunchKernelGGL(sort_rows_kernel<CHUNK>, grid, dim3(256), 0, st, slots, experts, expert_idx, counts, row_of_slot, split_sizes);
+  };
+  if (sort_chunk(slots) == 1024) sort(std::integral_constant<int, 1024>{});
+  else sort(std::integral_constant<int, 4096>{});
+  if (x) {
+    with_unit(dtype, wide, [&](auto e, auto n) {
       typedef decltype(e) T;
       constexpr int V = decltype(n)::value;
       a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
       const int64_t per = 256 >> a.tpt_log2;
-      hipLaunchKernelGGL((scatter_kernel<T, V>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a, row_of_slot,
-                         static_cast<const T*>(x), weights, static_cast<T*>(rows), row_weights);
+      with_topk(topk, [&](auto k) {
+        hipLaunchKernelGGL((scatter_kernel<T, V, decltype(k)::value>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a,
+                           row_of_slot, static_cast<const T*>(x), weights, static_cast<T*>(rows), row_weights);
+      });
     });
   }
   return launched();
@@ -660,8 +849,10 @@ static int combine_call(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
     constexpr int V = decltype(n)::value;
     a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
     const int64_t per = 256 >> a.tpt_log2;
-    hipLaunchKernelGGL((combine_kernel<T, V>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a, row_of_slot,
-                       static_cast<const T*>(rows), weights, static_cast<T*>(y), drow_weights, dweights);
+    with_topk(topk, [&](auto k) {
+      hipLaunchKernelGGL((combine_kernel<T, V, decltype(k)::value>), dim3((unsigned)((tokens + per - 1) / per)), dim3(256), 0, st, a,
+                         row_of_slot, static_cast<const T*>(rows), weights, static_cast<T*>(y), drow_weights, dweights);
+    });
   });
   return launched();
 }
@@ -691,8 +882,17 @@ int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
   with_unit(dtype, wide_rows(dtype, hidden, lddy, {dy, rows, drows}), [&](auto e, auto n) {
     typedef decltype(e) T;
     constexpr int V = decltype(n)::value;
-    hipLaunchKernelGGL((combine_bwd_kernel<T, V>), dim3((unsigned)tokens), dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(dy),
-                       static_cast<const T*>(rows), weights, static_cast<T*>(drows), dweights);
+    a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
+    const int64_t per = 256 >> a.tpt_log2;
+    const dim3 grid((unsigned)((tokens + per - 1) / per));
+    if (!weights && !dweights)  // without weights the gradient of the rows is a copy
+      with_topk(topk, [&](auto k) {
+        hipLaunchKernelGGL((scatter_kernel<T, V, decltype(k)::value>), grid, dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(dy),
+                           nullptr, static_cast<T*>(drows), nullptr);
+      });
+    else
+      hipLaunchKernelGGL((combine_bwd_kernel<T, V>), grid, dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(dy),
+                         static_cast<const T*>(rows), weights, static_cast<T*>(drows), dweights);
   });
   return launched();
 }

@@ -17,20 +17,25 @@ def _fail(msg, *args):
     raise ValueError(msg % args if args else msg)
 
 
-def _check(what, t, dtypes, ndim, device=None, contiguous=True):
+def _check(what, t, dtypes, ndim, device=None, contiguous=True, shape=None):
     """A CUDA tensor of one of `dtypes`, `ndim` dimensions and unit column stride (rows contiguous when
-    `contiguous`), on `device`."""
+    `contiguous`), on `device`, of `shape`."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and (device is None or t.device == device)
+            and (t.dim() == ndim if shape is None else t.shape == shape) and t.is_contiguous()):
+        return t
     if not isinstance(t, torch.Tensor):
         _fail("%s must be a tensor", what)
     if t.dtype not in dtypes:
         _fail("%s has type %s, expected %s", what, t.dtype, " or ".join(str(d) for d in dtypes))
     if t.dim() != ndim:
         _fail("%s has %d dimensions, expected %d", what, t.dim(), ndim)
-    if contiguous:
-        if not t.is_contiguous():
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _fail("%s has shape %s, expected %s", what, tuple(t.shape), tuple(shape))
+    if not t.is_contiguous():
+        if contiguous:
             _fail("%s must be contiguous", what)
-    elif t.numel() and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1):
-        _fail("%s must have unit column stride and rows that do not overlap (strides %s)", what, t.stride())
+        if t.numel() and (t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1):
+            _fail("%s must have unit column stride and rows that do not overlap (strides %s)", what, t.stride())
     if not t.is_cuda:
         _fail("%s must be on a GPU", what)
     if device is not None and t.device != device:
@@ -38,31 +43,21 @@ def _check(what, t, dtypes, ndim, device=None, contiguous=True):
     return t
 
 
-def _shape(what, t, shape):
-    if tuple(t.shape) != tuple(shape):
-        _fail("%s has shape %s, expected %s", what, tuple(t.shape), tuple(shape))
-
-
 def _ld(t):
     """Row stride in elements (a single row may carry any stride)."""
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-class _On:
-    """The tensors' device as the current one for the launch, and its stream handle."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guard = device, stream, None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return N._stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(device, stream, fn, *args):
+    """fn(*args, stream handle) with the tensors' device current, its error raised."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else N._stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, N._stream(stream))
+    if rc:
+        N._check(rc)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -85,14 +80,14 @@ def moe_route(logits, topk, score="softmax", renormalize=True, scale=1.0, expert
     dev = logits.device
     if expert_idx is None:
         expert_idx = torch.empty((t, topk), dtype=torch.int32, device=dev)
+    else:
+        _check("expert_idx", expert_idx, _I32, 2, dev, shape=(t, topk))
     if weights is None:
         weights = torch.empty((t, topk), dtype=torch.float32, device=dev)
-    _shape("expert_idx", _check("expert_idx", expert_idx, _I32, 2, dev), (t, topk))
-    _shape("weights", _check("weights", weights, _F32, 2, dev), (t, topk))
-    p = _params(score, renormalize, scale)
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_route(p, t, e, topk, logits.data_ptr(), N.DTYPE[logits.dtype], _ld(logits),
-                                     expert_idx.data_ptr(), weights.data_ptr(), s))
+    else:
+        _check("weights", weights, _F32, 2, dev, shape=(t, topk))
+    _call(dev, stream, N.LIB.mgs_moe_route, _params(score, renormalize, scale), t, e, topk, logits.data_ptr(),
+          N.DTYPE[logits.dtype], _ld(logits), expert_idx.data_ptr(), weights.data_ptr())
     return expert_idx, weights
 
 
@@ -103,15 +98,15 @@ def moe_route_bwd(logits, expert_idx, dweights, score="softmax", renormalize=Tru
     dev = logits.device
     _check("expert_idx", expert_idx, _I32, 2, dev)
     k = expert_idx.shape[1]
-    _shape("expert_idx", expert_idx, (t, k))
-    _shape("dweights", _check("dweights", dweights, _F32, 2, dev), (t, k))
+    if expert_idx.shape[0] != t:
+        _fail("expert_idx has %d rows, expected %d", expert_idx.shape[0], t)
+    _check("dweights", dweights, _F32, 2, dev, shape=(t, k))
     if dlogits is None:
         dlogits = torch.empty((t, e), dtype=logits.dtype, device=dev)
-    _shape("dlogits", _check("dlogits", dlogits, (logits.dtype,), 2, dev, contiguous=False), (t, e))
-    p = _params(score, renormalize, scale)
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_route_bwd(p, t, e, k, logits.data_ptr(), N.DTYPE[logits.dtype], _ld(logits),
-                                         expert_idx.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _ld(dlogits), s))
+    else:
+        _check("dlogits", dlogits, (logits.dtype,), 2, dev, contiguous=False, shape=(t, e))
+    _call(dev, stream, N.LIB.mgs_moe_route_bwd, _params(score, renormalize, scale), t, e, k, logits.data_ptr(),
+          N.DTYPE[logits.dtype], _ld(logits), expert_idx.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _ld(dlogits))
     return dlogits
 
 
@@ -135,33 +130,34 @@ def moe_dispatch(expert_idx, num_experts, x=None, rows=None, weights=None, row_w
     need = moe_dispatch_workspace_bytes(t, k, num_experts)
     if row_of_slot is None:
         row_of_slot = torch.empty((t, k), dtype=torch.int32, device=dev)
+    else:
+        _check("row_of_slot", row_of_slot, _I32, 2, dev, shape=(t, k))
     if split_sizes is None:
         split_sizes = torch.empty(num_experts, dtype=torch.int64, device=dev)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _shape("row_of_slot", _check("row_of_slot", row_of_slot, _I32, 2, dev), (t, k))
-    _shape("split_sizes", _check("split_sizes", split_sizes, _I64, 1, dev), (num_experts,))
-    _check("workspace", workspace, (torch.uint8,), 1, dev)
+    else:
+        _check("split_sizes", split_sizes, _I64, 1, dev, shape=(num_experts,))
+    ws, wb = None, 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, wb = _check("workspace", workspace, (torch.uint8,), 1, dev).data_ptr(), workspace.numel()
     h, dt, ldx, xp, rp, n, wp, rwp = 0, 0, 0, None, None, 0, None, None
     if x is not None or rows is not None or weights is not None or row_weights is not None:
         if x is None or rows is None:
             _fail("x and rows go together (and weights need them)")
         _check("x", x, _FLOATS, 2, dev, contiguous=False)
-        _check("rows", rows, (x.dtype,), 2, dev)
-        h, dt, ldx, n = x.shape[1], N.DTYPE[x.dtype], _ld(x), rows.shape[0]
-        _shape("x", x, (t, h))
-        _shape("rows", rows, (n, h))
-        xp, rp = x.data_ptr(), rows.data_ptr()
+        h, n = x.shape[1], rows.shape[0]
+        if x.shape[0] != t:
+            _fail("x has %d rows, expected %d", x.shape[0], t)
+        _check("rows", rows, (x.dtype,), 2, dev, shape=(n, h))
+        dt, ldx, xp, rp = N.DTYPE[x.dtype], _ld(x), x.data_ptr(), rows.data_ptr()
         if (weights is None) != (row_weights is None):
             _fail("weights and row_weights go together")
         if weights is not None:
-            _shape("weights", _check("weights", weights, _F32, 2, dev), (t, k))
-            _shape("row_weights", _check("row_weights", row_weights, _F32, 1, dev), (n,))
-            wp, rwp = weights.data_ptr(), row_weights.data_ptr()
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_dispatch(t, k, num_experts, expert_idx.data_ptr(), h, dt, xp, ldx, wp, rp, n, rwp,
-                                        row_of_slot.data_ptr(), split_sizes.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel(), s))
+            wp = _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
+            rwp = _check("row_weights", row_weights, _F32, 1, dev, shape=(n,)).data_ptr()
+    _call(dev, stream, N.LIB.mgs_moe_dispatch, t, k, num_experts, expert_idx.data_ptr(), h, dt, xp, ldx, wp, rp, n, rwp,
+          row_of_slot.data_ptr(), split_sizes.data_ptr(), ws, wb)
     return row_of_slot, split_sizes
 
 
@@ -177,19 +173,18 @@ def moe_dispatch_bwd(row_of_slot, drows, drow_weights=None, dx=None, dweights=No
     t, k, h, n, dev = _slots_and_rows(row_of_slot, drows, "drows")
     if dx is None:
         dx = torch.empty((t, h), dtype=drows.dtype, device=dev)
-    _shape("dx", _check("dx", dx, (drows.dtype,), 2, dev, contiguous=False), (t, h))
+    else:
+        _check("dx", dx, (drows.dtype,), 2, dev, contiguous=False, shape=(t, h))
     dwp = gwp = None
     if drow_weights is not None:
-        _shape("drow_weights", _check("drow_weights", drow_weights, _F32, 1, dev), (n,))
+        gwp = _check("drow_weights", drow_weights, _F32, 1, dev, shape=(n,)).data_ptr()
         if dweights is None:
             dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
-        _shape("dweights", _check("dweights", dweights, _F32, 2, dev), (t, k))
-        gwp, dwp = drow_weights.data_ptr(), dweights.data_ptr()
+        dwp = _check("dweights", dweights, _F32, 2, dev, shape=(t, k)).data_ptr()
     elif dweights is not None:
         _fail("dweights needs drow_weights")
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_dispatch_bwd(t, k, h, N.DTYPE[drows.dtype], row_of_slot.data_ptr(), n, drows.data_ptr(),
-                                            gwp, dx.data_ptr(), _ld(dx), dwp, s))
+    _call(dev, stream, N.LIB.mgs_moe_dispatch_bwd, t, k, h, N.DTYPE[drows.dtype], row_of_slot.data_ptr(), n,
+          drows.data_ptr(), gwp, dx.data_ptr(), _ld(dx), dwp)
     return dx, dweights
 
 
@@ -199,12 +194,11 @@ def moe_combine(row_of_slot, rows, weights=None, y=None, stream=None):
     t, k, h, n, dev = _slots_and_rows(row_of_slot, rows)
     if y is None:
         y = torch.empty((t, h), dtype=rows.dtype, device=dev)
-    _shape("y", _check("y", y, (rows.dtype,), 2, dev, contiguous=False), (t, h))
-    if weights is not None:
-        _shape("weights", _check("weights", weights, _F32, 2, dev), (t, k))
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_combine(t, k, h, N.DTYPE[rows.dtype], row_of_slot.data_ptr(), n, rows.data_ptr(),
-                                       None if weights is None else weights.data_ptr(), y.data_ptr(), _ld(y), s))
+    else:
+        _check("y", y, (rows.dtype,), 2, dev, contiguous=False, shape=(t, h))
+    wp = None if weights is None else _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
+    _call(dev, stream, N.LIB.mgs_moe_combine, t, k, h, N.DTYPE[rows.dtype], row_of_slot.data_ptr(), n, rows.data_ptr(), wp,
+          y.data_ptr(), _ld(y))
     return y
 
 
@@ -217,24 +211,19 @@ def moe_combine_bwd(row_of_slot, dy, drows=None, rows=None, weights=None, dweigh
     t, k = row_of_slot.shape
     _check("dy", dy, _FLOATS, 2, dev, contiguous=False)
     h = dy.shape[1]
-    _shape("dy", dy, (t, h))
-    n = None
-    for name, v in (("drows", drows), ("rows", rows)):
-        if v is not None:
-            _check(name, v, (dy.dtype,), 2, dev)
-            n = v.shape[0] if n is None else n
-            _shape(name, v, (n, h))
-    if n is None:
+    if dy.shape[0] != t:
+        _fail("dy has %d rows, expected %d", dy.shape[0], t)
+    if drows is None and rows is None:
         _fail("drows or rows is needed")
+    n = (rows if drows is None else drows).shape[0]
+    rp = None if rows is None else _check("rows", rows, (dy.dtype,), 2, dev, shape=(n, h)).data_ptr()
+    dp = None if drows is None else _check("drows", drows, (dy.dtype,), 2, dev, shape=(n, h)).data_ptr()
+    wp = None if weights is None else _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
     if rows is not None and dweights is None:
         dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
-    for name, v in (("weights", weights), ("dweights", dweights)):
-        if v is not None:
-            _shape(name, _check(name, v, _F32, 2, dev), (t, k))
-    ptr = lambda v: None if v is None else v.data_ptr()
-    with _On(dev, stream) as s:
-        N._check(N.LIB.mgs_moe_combine_bwd(t, k, h, N.DTYPE[dy.dtype], row_of_slot.data_ptr(), n, dy.data_ptr(), _ld(dy),
-                                           ptr(rows), ptr(weights), ptr(drows), ptr(dweights), s))
+    dwp = None if dweights is None else _check("dweights", dweights, _F32, 2, dev, shape=(t, k)).data_ptr()
+    _call(dev, stream, N.LIB.mgs_moe_combine_bwd, t, k, h, N.DTYPE[dy.dtype], row_of_slot.data_ptr(), n, dy.data_ptr(),
+          _ld(dy), rp, wp, dp, dwp)
     return dweights
 
 
@@ -256,9 +245,8 @@ class MoELayer:
     def forward(self, x, logits):
         """x [tokens, hidden] BF16, logits [tokens, experts] BF16 or FP32 -> y [tokens, hidden] BF16."""
         _check("x", x, (torch.bfloat16,), 2, contiguous=False)
-        _check("logits", logits, _FLOATS, 2, x.device, contiguous=False)
-        _shape("logits", logits, (x.shape[0], self.mlp.e))
-        _shape("x", x, (x.shape[0], self.mlp.h))
+        _check("x", x, (torch.bfloat16,), 2, contiguous=False, shape=(x.shape[0], self.mlp.h))
+        _check("logits", logits, _FLOATS, 2, x.device, contiguous=False, shape=(x.shape[0], self.mlp.e))
         if x.shape[0] == 0:
             _fail("x has no tokens")
         cap = x.shape[0] * self.topk
@@ -278,7 +266,7 @@ class MoELayer:
         if c is None:
             _fail("backward() without a forward")
         row = c["row"]
-        _shape("dy", _check("dy", dy, (torch.bfloat16,), 2, row.device, contiguous=False), (row.shape[0], self.mlp.h))
+        _check("dy", dy, (torch.bfloat16,), 2, row.device, contiguous=False, shape=(row.shape[0], self.mlp.h))
         self.ctx = None
         with torch.cuda.device(dy.device):
             drows = torch.empty((row.numel(), self.mlp.h), dtype=torch.bfloat16, device=dy.device)

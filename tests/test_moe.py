@@ -77,9 +77,10 @@ def test_dispatch_and_combine_refusals():
     _refused(-2, dis(h=0, ldx=0), "hidden")
     _refused(-2, dis(ldx=63), "row stride")
     _refused(-1, dis(dt=5), "dtype")
-    need = lib.mgs_moe_dispatch_workspace_bytes(4, 2, 8)
-    _refused(-1, dis(wb=need - 1), "workspace")
-    _refused(-1, dis(ws=None), "workspace")
+    need = lib.mgs_moe_dispatch_workspace_bytes(4000, 2, 8)
+    assert need > 0
+    _refused(-1, dis(t=4000, n=8000, wb=need - 1), "workspace")
+    _refused(-1, dis(t=4000, n=8000, ws=None), "workspace")
     for bad in ((4, 0, 8), (4, 17, 8), (4, 2, 0), (4, 2, 257), (-1, 2, 8), (1 << 40, 2, 8)):
         assert lib.mgs_moe_dispatch_workspace_bytes(*bad) < 0
 
@@ -166,7 +167,7 @@ int main() {
     if (s < 0) {
       want(mgs_moe_route(&ok, 4, 8, 2, P, 0, s, I, F, nullptr));
       want(mgs_moe_dispatch(4, 2, 8, I, 64, 0, P, s, nullptr, P, 8, nullptr, I, L, P, 1 << 20, nullptr));
-      want(mgs_moe_dispatch(4, 2, 8, I, 64, 0, P, 64, nullptr, P, 8, nullptr, I, L, P, s, nullptr));
+      want(mgs_moe_dispatch(4000, 2, 8, I, 64, 0, P, 64, nullptr, P, 8000, nullptr, I, L, P, s, nullptr));
     }
   }
   for (int32_t c : counts) {
