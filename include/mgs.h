@@ -346,7 +346,9 @@ int mgs_grouped_col_sum(const mgs_groups* groups, int64_t width, const void* x_b
  * calls make both from a router's logits, and bring the expert outputs back into token order; nothing
  * leaves the device, so a captured graph follows each replay's routing (mgs_groups_update takes
  * split_sizes as it is written here).  A slot is one (token, choice) pair, numbered token * topk + choice.
- * Experts 1 .. MGS_MAX_GROUPS, topk 1 .. MGS_MAX_TOPK, tokens * topk below 2^31; tokens == 0 is allowed.
+ * Experts 1 .. MGS_MAX_GROUPS, topk 1 .. MGS_MAX_TOPK, tokens * topk below 2^31 and tokens such that a
+ * launch has fewer than 2^32 threads (up to 2^24 - 1 tokens always); tokens == 0 is allowed, and tensors without
+ * elements may be NULL.  An output must not be one of the call's inputs.
  * Every pointer is a DEVICE pointer but the params.  Results are deterministic. */
 
 typedef enum { MGS_SCORE_SOFTMAX = 0, MGS_SCORE_SIGMOID = 1 } mgs_score;
@@ -373,7 +375,7 @@ int mgs_moe_route(const mgs_route_params* params, int64_t tokens, int32_t expert
 
 /* The logits' gradient of the router's weights: dlogits [tokens x experts], of the logits' type, row
  * stride ld_dlogits, every element written (zeros where the formulas give none).  expert_idx is the
- * forward's; dweights [tokens x topk] FP32 (ignored where expert_idx is -1). */
+ * forward's (a token's experts are distinct); dweights [tokens x topk] FP32 (ignored where expert_idx is -1). */
 int mgs_moe_route_bwd(const mgs_route_params* params, int64_t tokens, int32_t experts, int32_t topk,
                       const void* logits, int32_t logits_dtype, int64_t ld, const int32_t* expert_idx,
                       const float* dweights, void* dlogits, int64_t ld_dlogits, void* stream);

@@ -6,6 +6,7 @@ pointers together with the current HIP stream.  There is no fallback: if the lib
 does not load, importing this module raises.
 """
 
+import array
 import ctypes
 import os
 
@@ -156,8 +157,8 @@ class _GroupsArg:
             self.arr = None
             self.struct = Groups(split_sizes.num_groups, None, split_sizes.max_rows, split_sizes.table.data_ptr())
         elif type(split_sizes) is list and all(type(m) is int for m in split_sizes):
-            self.arr = (ctypes.c_int64 * len(split_sizes))(*split_sizes)
-            self.struct = Groups(len(split_sizes), ctypes.addressof(self.arr), 0, None)
+            self.arr = array.array("q", split_sizes)
+            self.struct = Groups(len(split_sizes), self.arr.buffer_info()[0], 0, None)
         else:
             self.arr = np.ascontiguousarray(np.asarray(split_sizes, dtype=np.int64))
             self.struct = Groups(len(self.arr), self.arr.ctypes.data, 0, None)

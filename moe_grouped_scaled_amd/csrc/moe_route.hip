@@ -145,7 +145,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __rest
       sum = row_sum(sum);
     }
   } else if (pick >= 0) {
-    p = 1.0f / (1.0f + expf(-v));
+    const float z = expf(-fabsf(v));  // in (0, 1]: neither form below overflows
+    p = (v >= 0.0f ? 1.0f : z) / (1.0f + z);
   }
   if (a.renormalize) sum = row_sum(p);
   if (there && l < a.topk) {
@@ -683,6 +684,12 @@ void with_topk(int topk, F f) {
   else f(std::integral_constant<int, 16>{});
 }
 
+// A launch has at most 2^32 - 1 threads in a dimension.
+int check_blocks(int64_t blocks) {
+  if (blocks > UINT32_MAX / 256) return fail(MGS_ERR_SHAPE, "%lld workgroups: too many tokens for one call", (long long)blocks);
+  return MGS_OK;
+}
+
 // 16-byte units need whole units per row, aligned rows and aligned tensors
 bool wide_rows(int dtype, int64_t hidden, int64_t ld, std::initializer_list<const void*> ptrs) {
   const int n = dtype == MGS_DTYPE_BF16 ? 8 : 4;
@@ -692,10 +699,14 @@ bool wide_rows(int dtype, int64_t hidden, int64_t ld, std::initializer_list<cons
   return true;
 }
 
-int threads_per_token_log2(int64_t units) {
-  int k = 0;
-  while (k < 8 && ((int64_t)1 << k) < units) ++k;
-  return k;
+// Threads per token and the launch's workgroups, for rows moved in 16-byte units or single elements.
+int set_grid(MoveArgs* a, int dtype, bool wide, int64_t* blocks) {
+  const int64_t v = wide ? (dtype == MGS_DTYPE_BF16 ? 8 : 4) : 1, units = (a->hidden + v - 1) / v;
+  a->tpt_log2 = 0;
+  while (a->tpt_log2 < 8 && ((int64_t)1 << a->tpt_log2) < units) ++a->tpt_log2;
+  const int64_t per = 256 >> a->tpt_log2;
+  *blocks = (a->tokens + per - 1) / per;
+  return check_blocks(*blocks);
 }
 
 int check_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, int32_t topk, const void* logits,
@@ -756,6 +767,7 @@ int mgs_moe_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, i
   if (rc) return rc;
   if ((!expert_idx || !weights) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "expert_idx or weights is NULL");
   if (tokens == 0) return ok();
+  if ((rc = check_blocks((tokens + 15) / 16))) return rc;
   const dim3 grid((unsigned)((tokens + 15) / 16));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   with_experts(experts, [&](auto n) {
@@ -777,6 +789,8 @@ int mgs_moe_route_bwd(const mgs_route_params* rp, int64_t tokens, int32_t expert
   if ((!expert_idx || !dweights || !dlogits) && tokens > 0)
     return fail(MGS_ERR_INVALID_ARG, "expert_idx, dweights or dlogits is NULL");
   if (tokens == 0) return ok();
+  if (dlogits == logits) return fail(MGS_ERR_INVALID_ARG, "dlogits must not be the logits");
+  if ((rc = check_blocks((tokens + 15) / 16))) return rc;
   a.ldd = ld_dlogits;
   const dim3 grid((unsigned)((tokens + 15) / 16));
   const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -812,7 +826,7 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
   if (x || rows || weights || row_weights) {
     if ((rc = check_move(tokens, topk, hidden, dtype, ldx, num_rows, &a))) return rc;
     if ((!x || !rows) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "x and rows go together");
-    if ((weights == nullptr) != (row_weights == nullptr))
+    if (tokens > 0 && (weights == nullptr) != (row_weights == nullptr))
       return fail(MGS_ERR_INVALID_ARG, "weights and row_weights go together");
     if (num_rows < slots)
       return fail(MGS_ERR_SHAPE, "rows has %lld rows, %lld tokens x topk %d can need %lld", (long long)num_rows, (long long)tokens, topk, (long long)slots);
@@ -823,8 +837,12 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(MGS_ERR_INVALID_ARG, "the sort needs a workspace of %lld bytes (got %lld%s)", (long long)need,
                 (long long)workspace_bytes, workspace ? "" : ", NULL");
-  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (tokens > 0 && (row_of_slot == expert_idx || (x && x == rows)))
+    return fail(MGS_ERR_INVALID_ARG, "row_of_slot and rows must not be expert_idx and x");
   const bool wide = x && wide_rows(dtype, hidden, ldx, {x, rows});
+  int64_t blocks = 0;
+  if (x && (rc = set_grid(&a, dtype, wide, &blocks))) return rc;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
   a.experts = experts;
   a.topk = topk;
   a.tokens = tokens;
@@ -852,12 +870,10 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
     with_unit(dtype, wide, [&](auto e, auto n) {
       typedef decltype(e) T;
       constexpr int V = decltype(n)::value;
-      a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
-      const int64_t per = 256 >> a.tpt_log2;
       with_flag(V > 1 && streams(tokens, topk, hidden, dtype), [&](auto nt) {
         with_topk(topk, [&](auto k) {
-          hipLaunchKernelGGL((scatter_kernel<T, V, decltype(k)::value, decltype(nt)::value>), dim3((unsigned)((tokens + per - 1) / per)),
-                             dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(x), weights, static_cast<T*>(rows), row_weights);
+          hipLaunchKernelGGL((scatter_kernel<T, V, decltype(k)::value, decltype(nt)::value>), dim3((unsigned)blocks), dim3(256), 0, st, a,
+                             row_of_slot, static_cast<const T*>(x), weights, static_cast<T*>(rows), row_weights);
         });
       });
     });
@@ -871,19 +887,21 @@ static int combine_call(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
   MoveArgs a;
   int rc = check_move(tokens, topk, hidden, dtype, ldy, num_rows, &a);
   if (rc) return rc;
-  if ((!row_of_slot || !rows || !y) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot, the rows or the token output is NULL");
-  if ((drow_weights == nullptr) != (dweights == nullptr))
+  if ((!row_of_slot || (!rows && num_rows > 0) || !y) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot, the rows or the token output is NULL");
+  if (tokens > 0 && num_rows > 0 && (drow_weights == nullptr) != (dweights == nullptr))
     return fail(MGS_ERR_INVALID_ARG, "drow_weights and dweights go together");
   if (tokens == 0) return ok();
+  if (rows == y) return fail(MGS_ERR_INVALID_ARG, "the token output must not be the rows");
+  const bool wide = wide_rows(dtype, hidden, ldy, {rows, y});
+  int64_t blocks;
+  if ((rc = set_grid(&a, dtype, wide, &blocks))) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  with_unit(dtype, wide_rows(dtype, hidden, ldy, {rows, y}), [&](auto e, auto n) {
+  with_unit(dtype, wide, [&](auto e, auto n) {
     typedef decltype(e) T;
     constexpr int V = decltype(n)::value;
-    a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
-    const int64_t per = 256 >> a.tpt_log2;
     with_flag(V > 1 && streams(tokens, topk, hidden, dtype), [&](auto nt) {
       with_topk(topk, [&](auto k) {
-        hipLaunchKernelGGL((combine_kernel<T, V, decltype(k)::value, decltype(nt)::value>), dim3((unsigned)((tokens + per - 1) / per)),
+        hipLaunchKernelGGL((combine_kernel<T, V, decltype(k)::value, decltype(nt)::value>), dim3((unsigned)blocks),
                            dim3(256), 0, st, a, row_of_slot, static_cast<const T*>(rows), weights, static_cast<T*>(y), drow_weights,
                            dweights);
       });
@@ -910,16 +928,21 @@ int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
   int rc = check_move(tokens, topk, hidden, dtype, lddy, num_rows, &a);
   if (rc) return rc;
   if ((!row_of_slot || !dy) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "row_of_slot or dy is NULL");
-  if (!drows && !dweights) return fail(MGS_ERR_INVALID_ARG, "no output requested (drows and dweights are NULL)");
-  if (dweights && !rows && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "dweights needs rows, the forward's input");
+  if (!drows && !dweights) {
+    if (tokens == 0 || num_rows == 0) return ok();  // (nothing to write, whatever was asked for)
+    return fail(MGS_ERR_INVALID_ARG, "no output requested (drows and dweights are NULL)");
+  }
+  if (dweights && !rows && tokens > 0 && num_rows > 0) return fail(MGS_ERR_INVALID_ARG, "dweights needs rows, the forward's input");
   if (tokens == 0) return ok();
+  if (drows && (drows == dy || drows == rows)) return fail(MGS_ERR_INVALID_ARG, "drows must not be dy or rows");
+  const bool wide = wide_rows(dtype, hidden, lddy, {dy, rows, drows});
+  int64_t blocks;
+  if ((rc = set_grid(&a, dtype, wide, &blocks))) return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  with_unit(dtype, wide_rows(dtype, hidden, lddy, {dy, rows, drows}), [&](auto e, auto n) {
+  with_unit(dtype, wide, [&](auto e, auto n) {
     typedef decltype(e) T;
     constexpr int V = decltype(n)::value;
-    a.tpt_log2 = threads_per_token_log2((hidden + V - 1) / V);
-    const int64_t per = 256 >> a.tpt_log2;
-    const dim3 grid((unsigned)((tokens + per - 1) / per));
+    const dim3 grid((unsigned)blocks);
     with_flag(V > 1 && streams(tokens, topk, hidden, dtype), [&](auto nt) {
       constexpr bool NT = decltype(nt)::value;
       if (!weights && !dweights) {  // without weights the gradient of the rows is a copy

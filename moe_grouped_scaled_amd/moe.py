@@ -1,8 +1,11 @@
 """Routing around the expert MLP: router, dispatch into expert order, combine, their gradients, and the layer.
 
 The functions check their tensors, allocate the outputs that are not given and enqueue the library's
-kernels on the tensors' device (its current stream, or `stream`).  Nothing synchronises: the split sizes
-stay in device memory, where `_native.DeviceGroups` takes them, so a captured graph follows the routing.
+kernels on the tensors' device, on its current stream.  With `stream` (a torch.cuda.Stream of that device
+or a HIP stream handle, 0 the null stream) they do as under ``torch.cuda.stream(stream)``: what they allocate
+belongs to that stream too.  Nothing synchronises: the split sizes stay in device memory, where
+`_native.DeviceGroups` takes them, so a captured graph follows the routing.  An output must not be one of
+the call's inputs.
 
 A slot is one (token, choice) pair, numbered token * topk + choice; a slot without an expert has expert -1
 and row -1.
@@ -48,16 +51,28 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
 
 
-def _call(device, stream, fn, *args):
+def _call(device, fn, *args):
     """fn(*args, stream handle) with the tensors' device current, its error raised."""
     index = device.index
     if index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else N._stream(stream))
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, N._stream(stream))
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         N._check(rc)
+
+
+def _on_stream(stream, t, fn, *args):
+    """fn(*args) with `stream` current; `t` is one of its tensors."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return fn(*args)  # refused there
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, t.device) if stream else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        _fail("the stream is on %s, the tensors are on %s", stream.device, t.device)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -75,6 +90,8 @@ def moe_route(logits, topk, score="softmax", renormalize=True, scale=1.0, expert
     ones by expert, and their weights: `scale` times the softmax over all experts or the sigmoid, divided
     by the picked ones' sum with `renormalize`.  Experts at -inf are never picked.  Returns
     (expert_idx int32, weights FP32), both [tokens, topk]."""
+    if stream is not None:
+        return _on_stream(stream, logits, moe_route, logits, topk, score, renormalize, scale, expert_idx, weights)
     _check("logits", logits, _FLOATS, 2, contiguous=False)
     t, e = logits.shape
     dev = logits.device
@@ -86,13 +103,15 @@ def moe_route(logits, topk, score="softmax", renormalize=True, scale=1.0, expert
         weights = torch.empty((t, topk), dtype=torch.float32, device=dev)
     else:
         _check("weights", weights, _F32, 2, dev, shape=(t, topk))
-    _call(dev, stream, N.LIB.mgs_moe_route, _params(score, renormalize, scale), t, e, topk, logits.data_ptr(),
+    _call(dev, N.LIB.mgs_moe_route, _params(score, renormalize, scale), t, e, topk, logits.data_ptr(),
           N.DTYPE[logits.dtype], _ld(logits), expert_idx.data_ptr(), weights.data_ptr())
     return expert_idx, weights
 
 
 def moe_route_bwd(logits, expert_idx, dweights, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
     """The logits' gradient of `moe_route`'s weights (every element of dlogits is written)."""
+    if stream is not None:
+        return _on_stream(stream, logits, moe_route_bwd, logits, expert_idx, dweights, score, renormalize, scale, dlogits)
     _check("logits", logits, _FLOATS, 2, contiguous=False)
     t, e = logits.shape
     dev = logits.device
@@ -105,7 +124,7 @@ def moe_route_bwd(logits, expert_idx, dweights, score="softmax", renormalize=Tru
         dlogits = torch.empty((t, e), dtype=logits.dtype, device=dev)
     else:
         _check("dlogits", dlogits, (logits.dtype,), 2, dev, contiguous=False, shape=(t, e))
-    _call(dev, stream, N.LIB.mgs_moe_route_bwd, _params(score, renormalize, scale), t, e, k, logits.data_ptr(),
+    _call(dev, N.LIB.mgs_moe_route_bwd, _params(score, renormalize, scale), t, e, k, logits.data_ptr(),
           N.DTYPE[logits.dtype], _ld(logits), expert_idx.data_ptr(), dweights.data_ptr(), dlogits.data_ptr(), _ld(dlogits))
     return dlogits
 
@@ -124,6 +143,9 @@ def moe_dispatch(expert_idx, num_experts, x=None, rows=None, weights=None, row_w
     tokens * topk rows; those past the last used one stay as they are.  Without `x` only the sort.  Returns
     (row_of_slot int32 [tokens, topk], split_sizes int64 [num_experts]).  A workspace given here must not be
     shared with a call that may run at the same time."""
+    if stream is not None:
+        return _on_stream(stream, expert_idx, moe_dispatch, expert_idx, num_experts, x, rows, weights, row_weights, row_of_slot, split_sizes,
+                          workspace)
     _check("expert_idx", expert_idx, _I32, 2)
     t, k = expert_idx.shape
     dev = expert_idx.device
@@ -156,7 +178,7 @@ def moe_dispatch(expert_idx, num_experts, x=None, rows=None, weights=None, row_w
         if weights is not None:
             wp = _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
             rwp = _check("row_weights", row_weights, _F32, 1, dev, shape=(n,)).data_ptr()
-    _call(dev, stream, N.LIB.mgs_moe_dispatch, t, k, num_experts, expert_idx.data_ptr(), h, dt, xp, ldx, wp, rp, n, rwp,
+    _call(dev, N.LIB.mgs_moe_dispatch, t, k, num_experts, expert_idx.data_ptr(), h, dt, xp, ldx, wp, rp, n, rwp,
           row_of_slot.data_ptr(), split_sizes.data_ptr(), ws, wb)
     return row_of_slot, split_sizes
 
@@ -170,6 +192,8 @@ def _slots_and_rows(row_of_slot, rows, name="rows"):
 def moe_dispatch_bwd(row_of_slot, drows, drow_weights=None, dx=None, dweights=None, stream=None):
     """Gradient of the dispatch: dx[t] = the sum of the token's drows, and with `drow_weights` (FP32, one a row)
     dweights[t, c] = drow_weights[row_of_slot[t, c]].  Returns (dx, dweights or None)."""
+    if stream is not None:
+        return _on_stream(stream, row_of_slot, moe_dispatch_bwd, row_of_slot, drows, drow_weights, dx, dweights)
     t, k, h, n, dev = _slots_and_rows(row_of_slot, drows, "drows")
     if dx is None:
         dx = torch.empty((t, h), dtype=drows.dtype, device=dev)
@@ -183,7 +207,7 @@ def moe_dispatch_bwd(row_of_slot, drows, drow_weights=None, dx=None, dweights=No
         dwp = _check("dweights", dweights, _F32, 2, dev, shape=(t, k)).data_ptr()
     elif dweights is not None:
         _fail("dweights needs drow_weights")
-    _call(dev, stream, N.LIB.mgs_moe_dispatch_bwd, t, k, h, N.DTYPE[drows.dtype], row_of_slot.data_ptr(), n,
+    _call(dev, N.LIB.mgs_moe_dispatch_bwd, t, k, h, N.DTYPE[drows.dtype], row_of_slot.data_ptr(), n,
           drows.data_ptr(), gwp, dx.data_ptr(), _ld(dx), dwp)
     return dx, dweights
 
@@ -191,13 +215,15 @@ def moe_dispatch_bwd(row_of_slot, drows, drow_weights=None, dx=None, dweights=No
 def moe_combine(row_of_slot, rows, weights=None, y=None, stream=None):
     """y[t] = the sum over the token's slots of weights[t, c] * rows[row_of_slot[t, c]] (weights 1 when None),
     in FP32 with one rounding."""
+    if stream is not None:
+        return _on_stream(stream, row_of_slot, moe_combine, row_of_slot, rows, weights, y)
     t, k, h, n, dev = _slots_and_rows(row_of_slot, rows)
     if y is None:
         y = torch.empty((t, h), dtype=rows.dtype, device=dev)
     else:
         _check("y", y, (rows.dtype,), 2, dev, contiguous=False, shape=(t, h))
     wp = None if weights is None else _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
-    _call(dev, stream, N.LIB.mgs_moe_combine, t, k, h, N.DTYPE[rows.dtype], row_of_slot.data_ptr(), n, rows.data_ptr(), wp,
+    _call(dev, N.LIB.mgs_moe_combine, t, k, h, N.DTYPE[rows.dtype], row_of_slot.data_ptr(), n, rows.data_ptr(), wp,
           y.data_ptr(), _ld(y))
     return y
 
@@ -206,6 +232,8 @@ def moe_combine_bwd(row_of_slot, dy, drows=None, rows=None, weights=None, dweigh
     """Gradient of the combine: drows[row_of_slot[t, c]] = weights[t, c] * dy[t] (rows no slot has stay as they
     are), and with `rows`, the forward's input, dweights[t, c] = <dy[t], rows[row_of_slot[t, c]]>, which is
     returned (else None)."""
+    if stream is not None:
+        return _on_stream(stream, row_of_slot, moe_combine_bwd, row_of_slot, dy, drows, rows, weights, dweights)
     _check("row_of_slot", row_of_slot, _I32, 2)
     dev = row_of_slot.device
     t, k = row_of_slot.shape
@@ -222,7 +250,7 @@ def moe_combine_bwd(row_of_slot, dy, drows=None, rows=None, weights=None, dweigh
     if rows is not None and dweights is None:
         dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
     dwp = None if dweights is None else _check("dweights", dweights, _F32, 2, dev, shape=(t, k)).data_ptr()
-    _call(dev, stream, N.LIB.mgs_moe_combine_bwd, t, k, h, N.DTYPE[dy.dtype], row_of_slot.data_ptr(), n, dy.data_ptr(),
+    _call(dev, N.LIB.mgs_moe_combine_bwd, t, k, h, N.DTYPE[dy.dtype], row_of_slot.data_ptr(), n, dy.data_ptr(),
           _ld(dy), rp, wp, dp, dwp)
     return dweights
 
