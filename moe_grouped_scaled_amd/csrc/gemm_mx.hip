@@ -1225,7 +1225,7 @@ GemmVariant mxfp4_variant(const GemmArgs& ga, const GroupTable& gt) {
     for (int g = 0; g < gt.num_groups; ++g) most = std::max<int64_t>(most, gt.row_off[g + 1] - gt.row_off[g]);
   }
   // (a tile's 256 rows of 2^24 elements span 2^31 bytes, one more than its descriptor covers)
-  if (most > 64 && ga.k < (int64_t)1 << 24 && count_tiles(ga, gt, BM2, BN2) > 128) return {gemm_mxfp4_256_kernel, BM2, BN2};
+  if (most > 64 && ga.k < (int64_t)1 << 24 && count_tiles(ga, gt, BM2, BN2) > 128) return {ga.c_f32 ? gemm_mxfp4_256_kernel<true> : gemm_mxfp4_256_kernel<false>, BM2, BN2};
   const int64_t fill = 512;
   if (most <= 16) {
     if (count_tiles(ga, gt, 16, 32) >= fill) return {gemm_mxfp4_rows_kernel<1, 2, 1>, 16, 32};

@@ -204,58 +204,71 @@ __device__ __forceinline__ void mfma_scale_fp4(v16f& acc, const v4i& b, const v4
 }
 
 // Epilogue: lane (r32, h32) of wave (wm, wn) holds, for fragment (fm, fn) and register group g, output row
-// 128 wm + 32 fm + r32 and the four columns 128 wn + 32 fn + 8 g + 4 h32 .. + 3.  BF16: a lane swap
-// between the halves for a pair of groups gives every lane eight consecutive columns, one 16-byte store.
-// Whole fragments are in or out by column (N % 32 == 0), rows are masked once per fragment row, and the
-// addresses are a wave-uniform base and one 32-bit lane offset.
-template <bool F32, bool ACC, bool BIAS>
-__device__ __forceinline__ void epilogue_fp4(const TileJob& j, v16f (&acc)[4][4], const uint2* bias_lds, int wm, int wn,
-                                             int r32, int h32) {
-  const uint32_t lane_off = (uint32_t)r32 * (uint32_t)j.ldc + (F32 ? 4u : 8u) * (uint32_t)h32;
+// 128 wm + 32 fm + r32 and the four columns 128 wn + 32 fn + 8 g + 4 h32 .. + 3.  Stored from there, an
+// instruction would write 32 bytes of each of 32 rows; 32 rows at a time go through the wave's part of LDS
+// instead (free by then) and leave it as whole 256-byte (FP32: 512-byte) row pieces, non-temporal: the
+// outputs of the tiles in flight fill the L2, and the operands are read again.  16 x 2048 x 4096 x 4096: 288 us
+// (331 from the fragments, 317 through LDS with plain stores); its weight gradient in FP32 407 us (560, 470).
+template <bool F32>
+__device__ __forceinline__ void epilogue_fp4(const TileJob& j, v16f (&acc)[4][4], const uint2* bias_lds, uint8_t* buf,
+                                             bool accumulate, int wm, int wn, int lane) {
+  constexpr int STORE_NT = 2;  // cache policy of the buffer store
+  constexpr int ES = F32 ? 4 : 2, LPR = 128 * ES / 16, RPI = 64 / LPR;  // lanes per row, rows per instruction
+  constexpr int PITCH = 128 * ES + 16;  // the padding spreads the rows over the banks
+  const int r32 = lane & 31, h32 = lane >> 5, lr = lane / LPR, lc = lane % LPR;
+  const uint32_t ldb = (uint32_t)j.ldc * ES;
+  // columns past the tile's end: an offset past every record count
+  const uint32_t vo = wn * 128 * ES + 16 * lc < j.b.rows * ES ? (uint32_t)lr * ldb + 16u * (uint32_t)lc : 0x80000000u;
 #pragma unroll
   for (int fm = 0; fm < 4; ++fm) {
     const int row0 = wm * 128 + fm * 32;
-    if (row0 + r32 >= j.a.rows) continue;
-    const int64_t base = (j.crow0 + row0) * j.ldc + j.ccol0;
+    if (row0 >= j.a.rows) continue;
 #pragma unroll
     for (int fn = 0; fn < 4; ++fn) {
-      const int c0 = wn * 128 + fn * 32;
-      if (c0 >= j.b.rows) continue;
-      float v[4][4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        float v[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[g][t] = acc[fm][fn][4 * g + t];
-        if constexpr (BIAS) {
-          const uint2 bw = bias_lds[(c0 + 8 * g + 4 * h32) >> 2];
-          v[g][0] += bf16lo(bw.x); v[g][1] += bf16hi(bw.x); v[g][2] += bf16lo(bw.y); v[g][3] += bf16hi(bw.y);
-        }
-      }
-      if constexpr (F32) {
-        float* p = j.c32 + base + c0;
-        float4 o[4];
-        if constexpr (ACC) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) o[g] = *reinterpret_cast<const float4*>(p + lane_off + 8 * g);
-#pragma unroll
-          for (int g = 0; g < 4; ++g) { v[g][0] += o[g].x; v[g][1] += o[g].y; v[g][2] += o[g].z; v[g][3] += o[g].w; }
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          st16(p + lane_off + 8 * g, __float_as_uint(v[g][0]), __float_as_uint(v[g][1]), __float_as_uint(v[g][2]), __float_as_uint(v[g][3]));
-      } else {
-        uint16_t* p = j.c16 + base + c0;
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          const U2 x = swap32(bf16x2(v[g][0], v[g][1]), bf16x2(v[g + 1][0], v[g + 1][1]));
-          const U2 y = swap32(bf16x2(v[g][2], v[g][3]), bf16x2(v[g + 1][2], v[g + 1][3]));
-          st16(p + lane_off + 8 * g, x.x, y.x, x.y, y.y);
-        }
+        for (int t = 0; t < 4; ++t) v[t] = acc[fm][fn][4 * g + t];
+        const uint2 bw = bias_lds[(wn * 128 + fn * 32 + 8 * g + 4 * h32) >> 2];
+        v[0] += bf16lo(bw.x); v[1] += bf16hi(bw.x); v[2] += bf16lo(bw.y); v[3] += bf16hi(bw.y);
+        uint8_t* p = buf + r32 * PITCH + ES * (fn * 32 + 8 * g + 4 * h32);
+        if constexpr (F32) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
       }
     }
+    // a wave's LDS accesses execute in order; this keeps the compiler's order
+    asm volatile("" ::: "memory");
+    const int64_t at = (j.crow0 + row0) * j.ldc + j.ccol0 + wn * 128;
+    void* base = F32 ? static_cast<void*>(j.c32 + at) : static_cast<void*>(j.c16 + at);
+    const int64_t bytes = (int64_t)std::min(j.a.rows - row0, 32) * j.ldc * ES;
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)std::min<int64_t>(bytes, 0x7fffffff), RSRC_WORD3);
+    constexpr int BATCH = 8;
+#pragma unroll
+    for (int i0 = 0; i0 < 32 / RPI; i0 += BATCH) {
+      v4u w[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) w[i] = *reinterpret_cast<const v4u*>(buf + (RPI * (i0 + i) + lr) * PITCH + 16 * lc);
+      if (F32 && accumulate) {
+        v4u o[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) o[i] = __builtin_amdgcn_raw_buffer_load_b128(out, (int)(vo + (uint32_t)(RPI * (i0 + i)) * ldb), 0, 0);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) w[i][t] = __float_as_uint(__uint_as_float(w[i][t]) + __uint_as_float(o[i][t]));
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        __builtin_amdgcn_raw_buffer_store_b128(w[i], out, (int)(vo + (uint32_t)(RPI * (i0 + i)) * ldb), 0, STORE_NT);
+        asm volatile("s_nop 1" ::"v"(w[i]));
+      }
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
+template <bool F32>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * F4_STAGE];
@@ -417,7 +430,8 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
 
 #pragma unroll
   for (int n = 0; n < NLOADS; ++n) issue_one(0, smem, n);
-  if (d.has_bias && wave < 2) dma4(d.bias, (uint32_t)(wave * 256 + lane * 4), 0, lds_addr(bias_lds) + wave * 256);
+  // (without a bias zeros)
+  if (wave < 2) dma4(d.bias, d.has_bias ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u, 0, lds_addr(bias_lds) + wave * 256);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 #pragma unroll
@@ -432,14 +446,5 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   __builtin_amdgcn_sched_barrier(0);
   mfma_drain();
   __builtin_amdgcn_sched_barrier(0);
-  if (!j.c32) {
-    if (d.has_bias) epilogue_fp4<false, false, true>(j, acc, bias_lds, wm, wn, r32, h32);
-    else epilogue_fp4<false, false, false>(j, acc, bias_lds, wm, wn, r32, h32);
-  } else if (d.has_bias) {
-    if (ga.accumulate) epilogue_fp4<true, true, true>(j, acc, bias_lds, wm, wn, r32, h32);
-    else epilogue_fp4<true, false, true>(j, acc, bias_lds, wm, wn, r32, h32);
-  } else {
-    if (ga.accumulate) epilogue_fp4<true, true, false>(j, acc, bias_lds, wm, wn, r32, h32);
-    else epilogue_fp4<true, false, false>(j, acc, bias_lds, wm, wn, r32, h32);
-  }
+  epilogue_fp4<F32>(j, acc, bias_lds, smem + wave * (2 * F4_STAGE / 4), ga.accumulate != 0, wm, wn, lane);
 }
