@@ -317,14 +317,6 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
   };
 
   v16f acc[4][4];
-#pragma unroll
-  for (int fm = 0; fm < 4; ++fm)
-#pragma unroll
-    for (int fn = 0; fn < 4; ++fn) acc[fm][fn] = v16f{};
-  __builtin_amdgcn_sched_barrier(0);
-  mfma_valu_gap();
-  __builtin_amdgcn_sched_barrier(0);
-
   // fragment f of the wave's 128 rows: row 128 w + 32 f + r32; rows 32 f apart share the chunk swizzle
   const uint32_t ra = (uint32_t)(wm * 128 + r32) * F4_ROWB, rb = (uint32_t)(wn * 128 + r32) * F4_ROWB + F4_DATA;
   const uint32_t sa0 = 2 * F4_DATA + h32 * (BM2 * 4) + (wm * 128 + r32) * 4, sb0 = sa0 + F4_SC + (wn - wm) * 512;
@@ -391,8 +383,8 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
     uint8_t* stg = smem + (st & 1) * F4_STAGE;
     uint8_t* nxt = smem + ((st + 1) & 1) * F4_STAGE;
     const bool more = !TAIL && st + 1 < nsteps, more2 = !TAIL && st + 2 < nsteps;
-    auto feed = [&](int m) {  // m-th MFMA of the step's first three substeps
-      if (more && m % PACE == PACE - 1 && LEAD + m / PACE < NLOADS) issue_one(st + 1, nxt, LEAD + m / PACE);
+    auto feed = [&](int m) {  // m-th MFMA of the step's first three substeps (step 1 was loaded with step 0)
+      if (more && st > 0 && m % PACE == PACE - 1 && LEAD + m / PACE < NLOADS) issue_one(st + 1, nxt, LEAD + m / PACE);
     };
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
@@ -428,17 +420,26 @@ void gemm_mxfp4_256_kernel(GemmArgs ga, GemmTable tt) {
     }
   };
 
-#pragma unroll
-  for (int n = 0; n < NLOADS; ++n) issue_one(0, smem, n);
   // (without a bias zeros)
   if (wave < 2) dma4(d.bias, d.has_bias ? (uint32_t)(wave * 256 + lane * 4) : 0x80000000u, 0, lds_addr(bias_lds) + wave * 256);
-  __builtin_amdgcn_s_waitcnt(0);
+#pragma unroll
+  for (int n = 0; n < NLOADS; ++n) issue_one(0, smem, n);
+  if (nsteps > 1)
+#pragma unroll
+    for (int n = 0; n < NLOADS; ++n) issue_one(1, smem + F4_STAGE, n);
+  // (the accumulators are cleared while the loads are under way)
+#pragma unroll
+  for (int fm = 0; fm < 4; ++fm)
+#pragma unroll
+    for (int fn = 0; fn < 4; ++fn) acc[fm][fn] = v16f{};
+  __builtin_amdgcn_sched_barrier(0);
+  mfma_valu_gap();
+  __builtin_amdgcn_sched_barrier(0);
+  if (nsteps > 1) wait_loads<NLOADS>();
+  else wait_loads<0>();
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 16; ++i) read_one(smem, 0, 0, i);
-  if (nsteps > 1)
-#pragma unroll
-    for (int n = 0; n < LEAD; ++n) issue_one(1, smem + F4_STAGE, n);
   const bool tail = last_rem < F4_KSTEP;
   const int full = tail ? nsteps - 1 : nsteps;
   for (int st = 0; st < full; ++st) step(std::false_type{}, st);
