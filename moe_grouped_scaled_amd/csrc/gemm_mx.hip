@@ -1204,10 +1204,10 @@ int64_t count_tiles(const GemmArgs& ga, const GroupTable& gt, int tm, int tn) {
   return rows * ntn;
 }
 
-// MXFP4: which kernel and tile.  The 256 x 256 kernel needs tiles for half the CUs at least and groups of
-// more than 64 rows; below, a tile's time (26 us at K = 4096) stands alone: one expert x 256 rows, 4096 x
-// 4096 takes 28.9 us with it and 9.8 us in 512 tiles of 32 x 64, 1024 rows 29.7 and 22.3 us (64 x 64); 16
-// experts x 128 rows (256 tiles) 48.9 and 58 us; 16 experts x 64 rows 44.7 and 42.1 us.  The few-rows
+// MXFP4: which kernel and tile.  The 256 x 256 kernel needs groups of more than 64 rows and work for the chip:
+// below 1024 tiles of 64 x 64 a tile's own time (27 us at K = 4096) stands alone.  4096 x 4096, one expert x
+// 256, 1024, 2048 rows: 28.1, 29.6, 30.6 us with it and 9.1, 22.8, 41.1 us with the few-rows kernel; 8 experts
+// x 128, 256 rows 30.2, 30.3 and 25.3, 40.9 us; 16 experts x 64, 96 rows 36.4, 37.3 and 32.2, 44.9 us.  The few-rows
 // kernel takes the largest tile that still gives two workgroups per CU: 64 x 64 reads the weights once
 // for 64 rows, smaller ones fill the chip (one expert x 64 rows: 9.9 us in 64 x 64, 6.1 us in 32 x 32), and
 // no taller tile than the largest group needs (16 experts x 2 rows: 30.8 us with 16 x 32, 35.9 with 64 x 64).
@@ -1225,7 +1225,7 @@ GemmVariant mxfp4_variant(const GemmArgs& ga, const GroupTable& gt) {
     for (int g = 0; g < gt.num_groups; ++g) most = std::max<int64_t>(most, gt.row_off[g + 1] - gt.row_off[g]);
   }
   // (a tile's 256 rows of 2^24 elements span 2^31 bytes, one more than its descriptor covers)
-  if (most > 64 && ga.k < (int64_t)1 << 24 && count_tiles(ga, gt, BM2, BN2) > 128) return {ga.c_f32 ? gemm_mxfp4_256_kernel<true> : gemm_mxfp4_256_kernel<false>, BM2, BN2};
+  if (most > 64 && ga.k < (int64_t)1 << 24 && count_tiles(ga, gt, 64, 64) > 1024) return {ga.c_f32 ? gemm_mxfp4_256_kernel<true> : gemm_mxfp4_256_kernel<false>, BM2, BN2};
   const int64_t fill = 512;
   if (most <= 16) {
     if (count_tiles(ga, gt, 16, 32) >= fill) return {gemm_mxfp4_rows_kernel<1, 2, 1>, 16, 32};
