@@ -193,10 +193,12 @@ class QTensor:
         """`rht` (NVFP4 columnwise only): 16-bit sign mask of the Hadamard transform of the copy."""
         self.fmt, self.colwise, self.width = fmt, bool(colwise), int(width)
         self.rht = 0 if rht is None else RHT_ON | (int(rht) & 0xFFFF)
-        g, f = _GroupsArg(split_sizes), FMT[fmt]
-        nd, ns, ng = (LIB.mgs_qtensor_nbytes(f, int(self.colwise), g.ref, self.width, w) for w in (0, 1, 2))
-        if min(nd, ns, ng) < 0:
-            _check(int(min(nd, ns, ng)))
+        g, f, cw, nbytes = _GroupsArg(split_sizes), FMT[fmt], int(self.colwise), LIB.mgs_qtensor_nbytes
+        nd = nbytes(f, cw, g.ref, self.width, 0)
+        if nd < 0:
+            _check(int(nd))
+        ns = nbytes(f, cw, g.ref, self.width, 1)
+        ng = nbytes(f, cw, g.ref, self.width, 2) if fmt == "nvfp4" else 0
         self.data = torch.empty(nd, dtype=torch.uint8, device=device) if nd else torch.empty(1, dtype=torch.uint8, device=device)[:0]
         self.scales = torch.empty(ns, dtype=torch.uint8, device=device) if ns else torch.empty(1, dtype=torch.uint8, device=device)[:0]
         self.group_scale = torch.empty(ng // 4, dtype=torch.float32, device=device) if ng else None
