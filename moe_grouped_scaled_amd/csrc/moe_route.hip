@@ -26,6 +26,9 @@ namespace {
 // pick and nothing has to be marked as taken.  Replacing the last byte is exact for BF16 logits (and FP32
 // ones whose last byte is zero); for others a wave in which two neighbouring picks, or the last pick and
 // the next key, agree in the other 24 bits picks again with whole keys.
+//
+// Bound by the picks (VALU): 65536 tokens x 256 FP32 experts, top 8, takes 23 us for 67 MB of logits (13 us at
+// the rate of a large copy); 16 tokens x 32 experts 2.0 us, the shortest a launch is here.
 constexpr int ROUTE_LANES = 16;
 constexpr int DPP_ROW_ROR1 = 0x121, DPP_ROW_ROR2 = 0x122;
 
@@ -161,6 +164,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, const T* __rest
 // Gradient of the weights with respect to the logits.  Lane c of a token's sixteen holds choice c.  The
 // differences g_j - sum_i w_i g_i of the softmax and of the renormalization cancel where one weight is
 // near 1, so they are taken as sum_i w_i (g_j - g_i), plus g_j times the weight of the experts not picked.
+// Bound by bytes: 21 us at 65536 x 256, top 8, renormalized sigmoid (67 MB written, 6 MB of picks and gradients, and
+// a 64-byte piece of the logits per pick).
 template <typename T, int EPL>
 __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __restrict__ logits,
                                                         const int32_t* __restrict__ idx,
@@ -257,7 +262,7 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
 //
 // A stable counting sort of the slots by expert: row_of_slot[s] is the number of slots with a smaller
 // expert plus those with the same expert and a smaller number; slots without an expert get -1.  The
-// result is fixed by the indices alone.
+// result is fixed by the indices alone.  Two launches of 4.7 and 5.0 us at 32768 slots.
 
 // Slots per histogram block: at most 128 blocks up to 524288 slots, so that a block's sum over the
 // blocks before it stays short.
@@ -444,7 +449,8 @@ __device__ __forceinline__ int slot_row(const MoveArgs& a, const int32_t* __rest
   return r >= 0 && r < a.num_rows ? r : -1;
 }
 
-// x row of every token into the rows of its slots (the token's unit is read once)
+// x row of every token into the rows of its slots (the token's unit is read once).  Bound by bytes: 76 us for
+// 403 MB (16384 tokens x 4096, top 2: 5.3 TB/s, mostly writes).
 template <typename T, int V, int KMAX, bool NT>
 __device__ __forceinline__ void scatter_row(const MoveArgs& a, const int (&r)[KMAX], const T* __restrict__ x,
                                             T* __restrict__ rows, int u, int tpt) {
@@ -478,6 +484,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(MoveArgs a, const int32_t*
 
 // The whole dispatch in one launch, for few slots: a workgroup per token counts, over all slots, those that
 // precede each of its own in the sorted order, then copies its row.  Workgroup 0 also takes the split sizes.
+// 3.7 us for 8 tokens x 4096, top 2; the three launches of the general form take 12.
 template <typename T, int V, int KMAX, bool NT>
 __global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slots, const int32_t* __restrict__ idx,
                                                              const T* __restrict__ x, const float* __restrict__ weights,
@@ -524,7 +531,8 @@ __global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slo
 }
 
 // y of every token: the sum over its slots' rows in slot order, in FP32, with weights if given.  Row numbers
-// and weights are read once; the loads of eight rows go out before their sums.
+// and weights are read once; the loads of eight rows go out before their sums.  Bound by bytes: 67 us for 403 MB
+// (16384 tokens x 4096, top 2: 6.0 TB/s, mostly reads), 195 us for 1.06 GB (8192 x 7168, top 8).
 template <typename T, int V, int KMAX, bool NT>
 __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
                                                       const T* __restrict__ rows, const float* __restrict__ weights,
@@ -573,7 +581,9 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, const int32_t*
 }
 
 // d(rows) = w dy and d(w) = <dy, rows>, four slots of a token at a time: a unit of dy is read once for them.
-// The sums run over the token's threads by lane exchanges, then over its waves in order.
+// The sums run over the token's threads by lane exchanges, then over its waves in order.  10 us for 1021 tokens x
+// 1001 FP32, top 3 (23 MB): single elements, four dependent passes a row; with the passes' loads ahead of their
+// sums it took 9.5.
 template <typename T, int V, bool NT>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(MoveArgs a, const int32_t* __restrict__ row_of_slot,
                                                           const T* __restrict__ dy, const T* __restrict__ rows,
