@@ -23,7 +23,8 @@
  *   - Quantized widths (the quantized, contiguous dimension) must be multiples of 32, at most 2^24.
  *   - Size limits of the quantizing entry points (MGS_ERR_SHAPE beyond them): one group's columnwise
  *     matrix, roundup(m_g, 128) x W elements, stays below 2^31, and so does the byte size of the
- *     rowwise MXFP8 / MXFP4 scale array, 4 * M * ceil(W / 128).
+ *     rowwise MXFP8 / MXFP4 scale array, 4 * M * ceil(W / 128).  The MXFP4 grouped GEMM refuses operands
+ *     past them too.
  *   - Arithmetic follows IEEE FP32 with round-to-nearest-even; results are deterministic (no float
  *     atomics, fixed reduction orders).
  *

@@ -182,9 +182,11 @@ mgs::GemmTable* dev_gemm_table(const mgs_groups* groups) {
 
 
 // MXFP4 GEMM kernels address the scale arrays through 32-bit offsets: the rowwise scales of A (all rows)
-// and of the weights (all experts) stay below 2^31 bytes.
-int check_gemm_scales(int mode, int fmt, const mgs::GroupTable& gt, int64_t n, int64_t k) {
-  if (fmt != MGS_FMT_MXFP4 || mode == MGS_GEMM_WGRAD) return MGS_OK;
+// and of the weights (all experts) stay below 2^31 bytes.  The columnwise operands of a weight gradient have
+// the quantizing calls' limits.
+int check_gemm_scales(int mode, int fmt, const mgs::GroupTable& gt, int64_t m, int64_t n, int64_t k) {
+  if (fmt != MGS_FMT_MXFP4) return MGS_OK;
+  if (mode == MGS_GEMM_WGRAD) return check_extent(gt, std::max(m, n), "m or n");
   const int64_t rows = std::max<int64_t>(gt.total_rows, n * gt.num_groups);
   if (4 * rows * ((k + 127) / 128) >= (int64_t)1 << 31)
     return fail(MGS_ERR_SHAPE, "%lld rows x k %lld: a scale array reaches 2 GiB", (long long)rows, (long long)k);
@@ -492,7 +494,7 @@ int mgs_grouped_gemm_mx(int32_t mode, int32_t fmt, const mgs_groups* groups, int
     if ((rc = check_width(k, "k"))) return rc;
     if (m != rows) return fail(MGS_ERR_SHAPE, "m = %lld must equal the split sum %lld", (long long)m, (long long)rows);
   }
-  if ((rc = check_gemm_scales(mode, fmt, gt, n, k))) return rc;
+  if ((rc = check_gemm_scales(mode, fmt, gt, m, n, k))) return rc;
   mgs::GemmArgs ga{};
   ga.mode = mode;
   ga.fmt = fmt;

@@ -268,7 +268,9 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
 // blocks before it stays short.
 __host__ __device__ inline int sort_chunk(int64_t slots) { return slots <= 131072 ? 1024 : 4096; }
 
-// Up to this many slots the dispatch is one launch whose workgroups each look at all of them.
+// Up to this many slots the dispatch is one launch whose workgroups each look at all of them.  Replayed from a
+// graph, 4096 wide: 8 tokens x top 2 3.0 us (6.8 in the three launches of the general form), 64 x 4 4.3 (7.8),
+// 512 x 4 9.2 (10.6), 256 x 8 12.4 (11.5, but two launches more to enqueue).
 constexpr int64_t SMALL_SLOTS = 2048;
 
 __device__ __forceinline__ int slot_expert(const int32_t* __restrict__ idx, int64_t s, int64_t slots, int experts) {
@@ -484,7 +486,6 @@ __global__ __launch_bounds__(256) void scatter_kernel(MoveArgs a, const int32_t*
 
 // The whole dispatch in one launch, for few slots: a workgroup per token counts, over all slots, those that
 // precede each of its own in the sorted order, then copies its row.  Workgroup 0 also takes the split sizes.
-// 3.7 us for 8 tokens x 4096, top 2; the three launches of the general form take 12.
 template <typename T, int V, int KMAX, bool NT>
 __global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slots, const int32_t* __restrict__ idx,
                                                              const T* __restrict__ x, const float* __restrict__ weights,
