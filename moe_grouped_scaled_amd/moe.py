@@ -121,7 +121,7 @@ def moe_route_bwd(logits, expert_idx, dweights, score="softmax", renormalize=Tru
         _fail("expert_idx has %d rows, expected %d", expert_idx.shape[0], t)
     _check("dweights", dweights, _F32, 2, dev, shape=(t, k))
     if dlogits is None:
-        dlogits = torch.empty((t, e), dtype=logits.dtype, device=dev)
+        dlogits = logits.new_empty((t, e))
     else:
         _check("dlogits", dlogits, (logits.dtype,), 2, dev, contiguous=False, shape=(t, e))
     _call(dev, N.LIB.mgs_moe_route_bwd, _params(score, renormalize, scale), t, e, k, logits.data_ptr(),
@@ -151,7 +151,7 @@ def moe_dispatch(expert_idx, num_experts, x=None, rows=None, weights=None, row_w
     dev = expert_idx.device
     need = moe_dispatch_workspace_bytes(t, k, num_experts)
     if row_of_slot is None:
-        row_of_slot = torch.empty((t, k), dtype=torch.int32, device=dev)
+        row_of_slot = torch.empty_like(expert_idx)
     else:
         _check("row_of_slot", row_of_slot, _I32, 2, dev, shape=(t, k))
     if split_sizes is None:
@@ -196,14 +196,14 @@ def moe_dispatch_bwd(row_of_slot, drows, drow_weights=None, dx=None, dweights=No
         return _on_stream(stream, row_of_slot, moe_dispatch_bwd, row_of_slot, drows, drow_weights, dx, dweights)
     t, k, h, n, dev = _slots_and_rows(row_of_slot, drows, "drows")
     if dx is None:
-        dx = torch.empty((t, h), dtype=drows.dtype, device=dev)
+        dx = drows.new_empty((t, h))
     else:
         _check("dx", dx, (drows.dtype,), 2, dev, contiguous=False, shape=(t, h))
     dwp = gwp = None
     if drow_weights is not None:
         gwp = _check("drow_weights", drow_weights, _F32, 1, dev, shape=(n,)).data_ptr()
         if dweights is None:
-            dweights = torch.empty((t, k), dtype=torch.float32, device=dev)
+            dweights = drow_weights.new_empty((t, k))
         dwp = _check("dweights", dweights, _F32, 2, dev, shape=(t, k)).data_ptr()
     elif dweights is not None:
         _fail("dweights needs drow_weights")
@@ -219,7 +219,7 @@ def moe_combine(row_of_slot, rows, weights=None, y=None, stream=None):
         return _on_stream(stream, row_of_slot, moe_combine, row_of_slot, rows, weights, y)
     t, k, h, n, dev = _slots_and_rows(row_of_slot, rows)
     if y is None:
-        y = torch.empty((t, h), dtype=rows.dtype, device=dev)
+        y = rows.new_empty((t, h))
     else:
         _check("y", y, (rows.dtype,), 2, dev, contiguous=False, shape=(t, h))
     wp = None if weights is None else _check("weights", weights, _F32, 2, dev, shape=(t, k)).data_ptr()
