@@ -258,9 +258,12 @@ def moe_combine_bwd(row_of_slot, dy, drows=None, rows=None, weights=None, dweigh
 class MoELayer:
     """A mixture-of-experts layer from router logits to token outputs around an `ExpertMLP`.
 
-    forward(x, logits): route, dispatch with the weights as the rows' scales (the activation applies
-    them), the expert MLP with device-resident split sizes, combine.  backward(dy) returns the MLP's
-    gradients plus `dx` and `dlogits`; with the MLP's delay_wgrad its backward_dw() is still to be called.
+    forward(x, logits): y[t] = the sum over the token's experts of weight * expert(x[t]): route, dispatch, the
+    expert MLP with device-resident split sizes, combine.  Without an FC2 bias the weights go with the rows as
+    their scales (the activation applies them, FC2 is linear behind it).  With one they are applied by the
+    combine, so that they reach the bias too: the rows' scales are 1, and the expert outputs are kept for the
+    weights' gradient.  backward(dy) returns the MLP's gradients plus `dx` and `dlogits` (the latter with the
+    MLP's grad_probs); with the MLP's delay_wgrad its backward_dw() is still to be called.
     Row buffers are allocated for each step, tokens * topk rows each, so that a captured step keeps its
     own; rows behind the last used one are neither read nor written.
     """
@@ -281,11 +284,19 @@ class MoELayer:
         with torch.cuda.device(x.device):
             idx, w = moe_route(logits, self.topk, **self.route)
             rows = torch.empty((cap, self.mlp.h), dtype=torch.bfloat16, device=x.device)
-            probs = torch.empty(cap, dtype=torch.float32, device=x.device)
             groups = N.DeviceGroups(self.mlp.e, cap, device=x.device)
-            row, _ = moe_dispatch(idx, self.mlp.e, x, rows, weights=w, row_weights=probs, split_sizes=groups.splits)
-            y = moe_combine(row, self.mlp.forward(rows, probs, groups))
-        self.ctx = dict(logits=logits, idx=idx, row=row)
+            ctx = dict(logits=logits, idx=idx)
+            if self.mlp.b2 is None:
+                probs = torch.empty(cap, dtype=torch.float32, device=x.device)
+                row, _ = moe_dispatch(idx, self.mlp.e, x, rows, weights=w, row_weights=probs, split_sizes=groups.splits)
+                y = moe_combine(row, self.mlp.forward(rows, probs, groups))
+            else:
+                probs = torch.ones(cap, dtype=torch.float32, device=x.device)
+                row, _ = moe_dispatch(idx, self.mlp.e, x, rows, split_sizes=groups.splits)
+                y_rows = self.mlp.forward(rows, probs, groups)
+                y = moe_combine(row, y_rows, weights=w)
+                ctx.update(w=w, y_rows=y_rows if self.mlp.grad_probs else None)
+        self.ctx = dict(ctx, row=row)
         return y
 
     def backward(self, dy):
@@ -298,12 +309,17 @@ class MoELayer:
         self.ctx = None
         with torch.cuda.device(dy.device):
             drows = torch.empty((row.numel(), self.mlp.h), dtype=torch.bfloat16, device=dy.device)
-            moe_combine_bwd(row, dy, drows)
+            if "w" in c:  # the combine's weights
+                dw = moe_combine_bwd(row, dy, drows, rows=c["y_rows"], weights=c["w"])
+            else:
+                dw = moe_combine_bwd(row, dy, drows)
             grads = self.mlp.backward(drows)
             dx_rows, dprobs = grads.pop("dx1", None), grads.pop("dprobs", None)
-            dw = None
+            if "w" in c:
+                dprobs = None  # of the rows' scales of 1
             if dx_rows is not None:
-                grads["dx"], dw = moe_dispatch_bwd(row, dx_rows, drow_weights=dprobs)
+                grads["dx"], got = moe_dispatch_bwd(row, dx_rows, drow_weights=dprobs)
+                dw = got if dw is None else dw
             elif dprobs is not None:
                 # the tokens need no gradient: every slot fetches its row's scale gradient
                 dw, _ = moe_dispatch_bwd(row.view(-1, 1), dprobs.view(-1, 1))

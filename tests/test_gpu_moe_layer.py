@@ -1,0 +1,234 @@
+"""The mixture-of-experts layer against its definition in 64 bits, y[t] = sum_j w_tj E_j(x[t]) with
+E(x) = W2 act(W1 x + b1) + b2, and against its parts, with and without an FC2 bias (which the router's weights
+scale like the rest of the expert's output).
+
+The definition is met exactly where nothing rounds: small integers in x, biases and gradients, signed
+permutations as weights, the identity activation.  Every quantized block then holds small integers (or halves)
+that E4M3 and E2M1 elements under a power-of-two scale represent, BF16 holds the experts' outputs, and FP32 their
+sums.  What is left are the router's weights and the roundings named at each bound (u = 2^-24)."""
+
+import numpy as np
+import pytest
+
+import workloads
+from tests.helpers import bf16_f64, bf16_host, f32, to_dev, to_dev_bf16
+from tests.test_gpu_moe import _grad64, _route64, _sorted64
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+T, E, K, H = 150, 4, 2, 128
+
+
+@pytest.fixture(scope="module")
+def M():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import moe_grouped_scaled_amd
+    return moe_grouped_scaled_amd
+
+
+def _dev16(v):
+    return to_dev_bf16(workloads.bf16_bits(v.astype(np.float32)))
+
+
+def _exact_layer(M, fmt, bias, seed, route=None, **kw):
+    """A layer of signed permutations and integer biases, and its 64-bit weights."""
+    from moe_grouped_scaled_amd.expert_mlp import ExpertMLP
+    rng = np.random.default_rng(seed)
+    perm = lambda: np.stack([np.eye(H)[rng.permutation(H)] * rng.choice((-1.0, 1.0), (H, 1)) for _ in range(E)])
+    w1, w2, b1 = perm(), perm(), rng.integers(-1, 2, (E, H)).astype(np.float64)
+    b2 = rng.integers(-8, 9, (E, H)) / 4.0 if bias else None
+    mlp = ExpertMLP("identity", fmt, _dev16(w1), _dev16(w2), _dev16(b1), None if b2 is None else _dev16(b2), **kw)
+    return M.MoELayer(mlp, K, **(route or {})), w1, b1, w2, np.zeros((E, H)) if b2 is None else b2
+
+
+def _data(rng, masked):
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    if masked:
+        logits[::17] = -np.inf                    # tokens without any expert
+        logits[5::23, 1:] = -np.inf               # one expert for two choices
+        logits[:, 2] = -np.inf                    # an expert without tokens
+    return rng.integers(-3, 4, (T, H)).astype(np.float64), logits, rng.integers(-3, 4, (T, H)).astype(np.float64)
+
+
+def _experts64(x, w1, b1, w2, b2):
+    """Hidden values and outputs of every expert for every token: [T, E, H] each."""
+    a = np.einsum("th,efh->tef", x, w1) + b1
+    return a, np.einsum("tef,ehf->teh", a, w2) + b2
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_output_and_weight_dependent_gradients(M, fmt, bias, score, renorm):
+    """y, db2 and dlogits with the router's own weights."""
+    import torch
+    layer, w1, b1, w2, b2 = _exact_layer(M, fmt, bias, 3, dict(score=score, renormalize=renorm))
+    x, logits, dy = _data(np.random.default_rng(4), True)
+    y = layer.forward(_dev16(x), to_dev(logits))
+    g = layer.backward(_dev16(dy))
+    torch.cuda.synchronize()
+    idx, order, live, p, w, d = _route64(logits.astype(np.float64), K, score, renorm, 1.0)
+    a, out = _experts64(x, w1, b1, w2, b2)
+    picked = np.take_along_axis(out, order[:, :, None], 1)
+    ref, size = (w[:, :, None] * picked).sum(1), (w[:, :, None] * np.abs(picked)).sum(1)
+    wt = (np.max(d, 1, keepdims=True) + E + 8) * 2 * U     # the weights' own error
+    if bias:
+        # weights at the combine: their error, K products and sums, one rounding
+        bound = (wt + (K + 2) * U) * size + 2.0 ** -8 * np.abs(ref)
+    else:
+        # weights in the activation: each product with them is rounded to an element of a block.  E4M3: half a
+        # step 2^-4 of the value, or saturation, 448 for up to 512, 2^-3; E2M1: steps of a quarter of the
+        # scale and up, saturation 6 for up to 8: a quarter of the value, or an eighth of the block's maximum 4
+        q = picked - b2[np.where(live, order, 0)]
+        rel, of_max = (2.0 ** -3, 2.0 ** -17) if fmt == "mxfp8" else (2.0 ** -2, 2.0 ** -3)
+        err = (w[:, :, None] * (np.abs(q) * rel + 4.0 * of_max)).sum(1) + (wt + (K + 2) * U) * size
+        # and BF16 roundings of the experts' outputs and of the sum
+        bound = err + (2.0 ** -8 + 2.0 ** -8) * (size + err)
+    got = bf16_f64(bf16_host(y))
+    assert np.all(np.abs(got - ref) <= bound)
+    if bias:
+        # column sums of the BF16 rows w dy: a rounding each, and as many FP32 sums as an expert has rows
+        for e in range(E):
+            we = (w * live * (order == e)).sum(1)
+            db, sz = we @ dy, we @ np.abs(dy)
+            assert np.all(np.abs(f32(g["db2"])[e] - db) <= (2.0 ** -8 + np.max(wt) + 2 * T * U) * sz * 1.01), e
+        dw = np.where(live, (picked * dy[:, None, :]).sum(2), 0.0)  # exact in FP32: quarters below 2^22
+        want = _grad64(logits.astype(np.float64), order, live, p, dw, score, renorm, 1.0)
+        sz = np.abs(dw).sum(1, keepdims=True)
+        assert np.all(np.abs(f32(g["dlogits"]) - want) <= (2 * 8 + 2 * E + 4 * K + 24) * 4 * U * sz + 1e-36)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_exact_gradients(M, fmt, bias):
+    """Sigmoid weights of exactly 1/2 and 1: products of them with integers up to 4 are exact too (the activations'
+    rows then hold halves), so every output and gradient is the definition's."""
+    import torch
+    layer, w1, b1, w2, b2 = _exact_layer(M, fmt, bias, 5, dict(score="sigmoid", renormalize=False))
+    rng = np.random.default_rng(6)
+    x, logits, dy = _data(rng, True)
+    logits = np.where(np.isinf(logits), logits, np.where(rng.random((T, E)) < 0.5, 0.0, 20.0)).astype(np.float32)
+    y = layer.forward(_dev16(x), to_dev(logits))
+    g = layer.backward(_dev16(dy))
+    torch.cuda.synchronize()
+    idx, order, live, _, _, _ = _route64(logits.astype(np.float64), K, "sigmoid", False, 1.0)
+    w = np.zeros((T, E))
+    for c in range(K):
+        r = np.flatnonzero(live[:, c])
+        w[r, order[r, c]] = np.where(logits[r, order[r, c]] > 0, 1.0, 0.5)
+    a, out = _experts64(x, w1, b1, w2, b2)
+    assert np.array_equal(bf16_f64(bf16_host(y)), (w[:, :, None] * out).sum(1))
+    dout = w[:, :, None] * dy[:, None, :]
+    da = np.einsum("teh,ehf->tef", dout, w2)
+    want = {"dw2": np.einsum("teh,tef->ehf", dout, a), "dw1": np.einsum("tef,th->efh", da, x), "db1": da.sum(0),
+            "db2": dout.sum(0)}
+    for k, v in want.items():
+        if k in g:
+            assert np.array_equal(f32(g[k]).reshape(v.shape), v), k
+    assert ("db2" in g) == bias
+    assert np.array_equal(bf16_f64(bf16_host(g["dx"])), np.einsum("tef,efh->th", da, w1))
+
+
+def test_logits_gradient_against_differences(M):
+    """Central differences of the 64-bit layer, step 1e-5, for tokens whose picks the step does not change: truncation
+    below 1e-9 of the loss's terms, cancellation 1e-10."""
+    import torch
+    layer, w1, b1, w2, b2 = _exact_layer(M, "mxfp8", True, 7)
+    x, logits, dy = _data(np.random.default_rng(8), False)
+    layer.forward(_dev16(x), to_dev(logits))
+    got = f32(layer.backward(_dev16(dy))["dlogits"])
+    torch.cuda.synchronize()
+    _, out = _experts64(x, w1, b1, w2, b2)
+    v = logits.astype(np.float64)
+    order = np.argsort(-v, axis=1, kind="stable")[:, :K]
+    picked = np.take_along_axis((out * dy[:, None, :]).sum(2), order, 1)  # <dy, E_j(x)>
+
+    def loss(z):
+        p = np.exp(np.take_along_axis(z, order, 1))
+        return (p * picked).sum(1) / p.sum(1)
+
+    top = -np.sort(-v, axis=1)
+    safe = (top[:, K - 1] - top[:, K]) > 1e-3
+    assert safe.sum() > T // 2
+    size = np.abs(picked).sum(1)
+    for e in range(E):
+        h = np.zeros_like(v)
+        h[:, e] = 1e-5
+        num = (loss(v + h) - loss(v - h)) / 2e-5
+        bound = ((2 * 8 + 2 * E + 4 * K + 24) * 4 * U + 1e-8) * size
+        assert np.all((np.abs(got[:, e] - num) <= bound)[safe]), e
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fmt,kind", [("mxfp8", "srelu"), ("mxfp4", "srelu"), ("mxfp4", "swiglu"), ("nvfp4", "srelu")])
+def test_layer_equals_its_parts(M, fmt, kind, bias):
+    """Against rows sorted by numpy and the expert MLP on host split sizes: bit for bit on the weights' gradients, sums
+    per token in 64 bits.  The weights are the rows' scales without an FC2 bias and the combine's with one."""
+    import torch
+    from moe_grouped_scaled_amd.expert_mlp import ExpertMLP
+
+    def mlp():
+        rng = np.random.default_rng(9)
+        f_in = 2 * H if kind == "swiglu" else H
+        w1, w2 = workloads.normal_bf16(rng, (E, f_in, H), 0.05), workloads.normal_bf16(rng, (E, H, H), 0.05)
+        b1, b2 = workloads.normal_bf16(rng, (E, f_in), 0.05), workloads.normal_bf16(rng, (E, H), 0.5)
+        return ExpertMLP(kind, fmt, to_dev_bf16(w1), to_dev_bf16(w2), to_dev_bf16(b1), to_dev_bf16(b2) if bias else None,
+                         recompute=True)
+
+    rng = np.random.default_rng(10)
+    _, logits, _ = _data(rng, True)
+    x, dy = to_dev_bf16(workloads.normal_bf16(rng, (T, H))), to_dev_bf16(workloads.normal_bf16(rng, (T, H)))
+    layer, ref = M.MoELayer(mlp(), K), mlp()
+    y = layer.forward(x, to_dev(logits))
+    g = layer.backward(dy)
+    torch.cuda.synchronize()
+    idx, order, live, p, _, _ = _route64(logits.astype(np.float64), K, "softmax", True, 1.0)
+    row, counts = _sorted64(idx, E)
+    there = row >= 0
+    n = int(counts.sum())
+    src, probs = np.empty(n, np.int64), np.empty(n, np.float32)
+    src[row[there]] = np.repeat(np.arange(T), K).reshape(T, K)[there]
+    _, wd = M.moe_route(to_dev(logits), K)
+    w = wd.cpu().numpy()
+    probs[row[there]] = w[there]
+    src, pd = torch.from_numpy(src).cuda(), to_dev(probs)
+    y_rows = ref.forward(x[src].contiguous(), torch.ones_like(pd) if bias else pd, counts.tolist())
+    drows = dy[src].contiguous()
+    want = ref.backward((drows.float() * pd[:, None]).to(torch.bfloat16) if bias else drows)
+    torch.cuda.synchronize()
+    for k in ("dw1", "dw2", "db1", "db2"):
+        assert (k in g) == (k in want) and (k not in g or torch.equal(g[k], want[k])), k
+    safe = np.maximum(row, 0)
+    for got, rows, ws in ((y, y_rows, w.astype(np.float64) if bias else np.ones_like(w)), (g["dx"], want["dx1"], np.ones_like(w))):
+        r = bf16_f64(bf16_host(rows))[safe] * (there * ws)[:, :, None]
+        ref64, size = r.sum(1), np.abs(r).sum(1)
+        assert np.all(np.abs(bf16_f64(bf16_host(got)) - ref64) <= (K + 2) * U * size + 2.0 ** -8 * np.abs(ref64))
+    if bias:  # dw = <dy, y_row>: H products in FP32
+        prod = (bf16_f64(bf16_host(y_rows))[safe] * bf16_f64(bf16_host(dy))[:, None, :])
+        dw, err = np.where(there, prod.sum(2), 0.0), (H + 2) * U * np.where(there, np.abs(prod).sum(2), 0.0)
+    else:
+        dw, err = np.where(there, f32(want["dprobs"])[safe], 0.0), np.zeros_like(w)
+    dref = _grad64(logits.astype(np.float64), order, live, p, dw, "softmax", True, 1.0)
+    size = np.abs(dw).sum(1, keepdims=True)
+    # w_e sum_i w_i (g_e - g_i) with weights up to 1: twice the largest error of g
+    assert np.all(np.abs(f32(g["dlogits"]) - dref) <= (2 * 8 + 2 * E + 4 * K + 24) * 4 * U * size + 2 * err.max(1, keepdims=True) + 1e-36)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_gradients_not_asked_for(M, bias):
+    """Without the tokens' gradient the logits' is the same; without the scales' there is none of the logits."""
+    import torch
+    x, logits, dy = _data(np.random.default_rng(11), True)
+    x, logits, dy = _dev16(x), to_dev(logits), _dev16(dy)
+    got = []
+    for kw in ({}, dict(grad_x1=False), dict(grad_probs=False), dict(grad_x1=False, grad_fc1=False, grad_fc2=False)):
+        layer = _exact_layer(M, "mxfp8", bias, 12, **kw)[0]
+        y = layer.forward(x, logits)
+        got.append(dict(layer.backward(dy), y=y))
+    torch.cuda.synchronize()
+    full, no_x, no_p, only_p = got
+    assert "dx" not in no_x and "dlogits" not in no_p and "dx" not in only_p and "dw1" not in only_p
+    for g in got[1:]:
+        assert all(torch.equal(v, full[k]) for k, v in g.items())
+    assert "dlogits" in no_x and "dlogits" in only_p and "dx" in no_p
