@@ -349,7 +349,8 @@ int mgs_grouped_col_sum(const mgs_groups* groups, int64_t width, const void* x_b
  * split_sizes as it is written here).  A slot is one (token, choice) pair, numbered token * topk + choice.
  * Experts 1 .. MGS_MAX_GROUPS, topk 1 .. MGS_MAX_TOPK, tokens * topk below 2^31 and tokens such that a
  * launch has fewer than 2^32 threads (up to 2^24 - 1 tokens always); tokens == 0 is allowed, and tensors without
- * elements may be NULL.  An output must not be one of the call's inputs.
+ * elements may be NULL.  An output (and the workspace) must not be or overlap another tensor of the call; this is
+ * refused as far as contiguous tensors and the first rows of strided ones show it.
  * Every pointer is a DEVICE pointer but the params.  Results are deterministic. */
 
 typedef enum { MGS_SCORE_SOFTMAX = 0, MGS_SCORE_SIGMOID = 1 } mgs_score;

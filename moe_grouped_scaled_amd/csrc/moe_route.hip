@@ -710,6 +710,34 @@ bool wide_rows(int dtype, int64_t hidden, int64_t ld, std::initializer_list<cons
   return true;
 }
 
+// Memory of a tensor of a call; of rows with a stride only the first, so that tensors side by side in one buffer
+// do not count as overlapping.
+struct Span {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+Span span(const char* name, const void* p, int64_t bytes) { return {name, p, p ? bytes : 0}; }
+Span span_rows(const char* name, const void* p, int64_t rows, int64_t width, int64_t ld, int dtype) {
+  const int64_t es = dtype == MGS_DTYPE_BF16 ? 2 : 4;
+  return span(name, p, (ld == width ? rows : std::min<int64_t>(rows, 1)) * width * es);
+}
+
+// No output may overlap another tensor of the call: workgroups read and write in any order.
+int check_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return fail(MGS_ERR_INVALID_ARG, "%s must not be or overlap %s", o->name, q->name);
+    for (const Span& i : ins)
+      if (meet(*o, i)) return fail(MGS_ERR_INVALID_ARG, "%s must not be or overlap %s", o->name, i.name);
+  }
+  return MGS_OK;
+}
+
 // Threads per token and the launch's workgroups, for rows moved in 16-byte units or single elements.
 int set_grid(MoveArgs* a, int dtype, bool wide, int64_t* blocks) {
   const int64_t v = wide ? (dtype == MGS_DTYPE_BF16 ? 8 : 4) : 1, units = (a->hidden + v - 1) / v;
@@ -779,6 +807,9 @@ int mgs_moe_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, i
   if ((!expert_idx || !weights) && tokens > 0) return fail(MGS_ERR_INVALID_ARG, "expert_idx or weights is NULL");
   if (tokens == 0) return ok();
   if ((rc = check_blocks((tokens + 15) / 16))) return rc;
+  if ((rc = check_overlap({span("expert_idx", expert_idx, tokens * topk * 4), span("weights", weights, tokens * topk * 4)},
+                          {span_rows("logits", logits, tokens, experts, ld, logits_dtype)})))
+    return rc;
   const dim3 grid((unsigned)((tokens + 15) / 16));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   with_experts(experts, [&](auto n) {
@@ -800,8 +831,11 @@ int mgs_moe_route_bwd(const mgs_route_params* rp, int64_t tokens, int32_t expert
   if ((!expert_idx || !dweights || !dlogits) && tokens > 0)
     return fail(MGS_ERR_INVALID_ARG, "expert_idx, dweights or dlogits is NULL");
   if (tokens == 0) return ok();
-  if (dlogits == logits) return fail(MGS_ERR_INVALID_ARG, "dlogits must not be the logits");
   if ((rc = check_blocks((tokens + 15) / 16))) return rc;
+  if ((rc = check_overlap({span_rows("dlogits", dlogits, tokens, experts, ld_dlogits, logits_dtype)},
+                          {span_rows("logits", logits, tokens, experts, ld, logits_dtype),
+                           span("expert_idx", expert_idx, tokens * topk * 4), span("dweights", dweights, tokens * topk * 4)})))
+    return rc;
   a.ldd = ld_dlogits;
   const dim3 grid((unsigned)((tokens + 15) / 16));
   const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -848,11 +882,16 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(MGS_ERR_INVALID_ARG, "the sort needs a workspace of %lld bytes (got %lld%s)", (long long)need,
                 (long long)workspace_bytes, workspace ? "" : ", NULL");
-  if (tokens > 0 && (row_of_slot == expert_idx || (x && x == rows)))
-    return fail(MGS_ERR_INVALID_ARG, "row_of_slot and rows must not be expert_idx and x");
   const bool wide = x && wide_rows(dtype, hidden, ldx, {x, rows});
   int64_t blocks = 0;
   if (x && (rc = set_grid(&a, dtype, wide, &blocks))) return rc;
+  // (rows past the slots are not written)
+  if ((rc = check_overlap({span("row_of_slot", row_of_slot, slots * 4), span("split_sizes", split_sizes, experts * (int64_t)8),
+                           span_rows("rows", rows, slots, hidden, hidden, dtype), span("row_weights", row_weights, slots * 4),
+                           span("the workspace", workspace, need)},
+                          {span("expert_idx", expert_idx, slots * 4), span_rows("x", x, tokens, hidden, ldx, dtype),
+                           span("weights", weights, slots * 4)})))
+    return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   a.experts = experts;
   a.topk = topk;
@@ -902,10 +941,14 @@ static int combine_call(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
   if (tokens > 0 && num_rows > 0 && (drow_weights == nullptr) != (dweights == nullptr))
     return fail(MGS_ERR_INVALID_ARG, "drow_weights and dweights go together");
   if (tokens == 0) return ok();
-  if (rows == y) return fail(MGS_ERR_INVALID_ARG, "the token output must not be the rows");
   const bool wide = wide_rows(dtype, hidden, ldy, {rows, y});
   int64_t blocks;
   if ((rc = set_grid(&a, dtype, wide, &blocks))) return rc;
+  const int64_t slots = tokens * topk;
+  if ((rc = check_overlap({span_rows("the token output", y, tokens, hidden, ldy, dtype), span("dweights", dweights, slots * 4)},
+                          {span("row_of_slot", row_of_slot, slots * 4), span_rows("the rows", rows, num_rows, hidden, hidden, dtype),
+                           span("weights", weights, slots * 4), span("drow_weights", drow_weights, num_rows * 4)})))
+    return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   with_unit(dtype, wide, [&](auto e, auto n) {
     typedef decltype(e) T;
@@ -945,10 +988,14 @@ int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
   }
   if (dweights && !rows && tokens > 0 && num_rows > 0) return fail(MGS_ERR_INVALID_ARG, "dweights needs rows, the forward's input");
   if (tokens == 0) return ok();
-  if (drows && (drows == dy || drows == rows)) return fail(MGS_ERR_INVALID_ARG, "drows must not be dy or rows");
   const bool wide = wide_rows(dtype, hidden, lddy, {dy, rows, drows});
   int64_t blocks;
   if ((rc = set_grid(&a, dtype, wide, &blocks))) return rc;
+  const int64_t slots = tokens * topk;
+  if ((rc = check_overlap({span_rows("drows", drows, num_rows, hidden, hidden, dtype), span("dweights", dweights, slots * 4)},
+                          {span("row_of_slot", row_of_slot, slots * 4), span_rows("dy", dy, tokens, hidden, lddy, dtype),
+                           span_rows("rows", rows, num_rows, hidden, hidden, dtype), span("weights", weights, slots * 4)})))
+    return rc;
   const hipStream_t st = static_cast<hipStream_t>(stream);
   with_unit(dtype, wide, [&](auto e, auto n) {
     typedef decltype(e) T;

@@ -4,8 +4,8 @@ The functions check their tensors, allocate the outputs that are not given and e
 kernels on the tensors' device, on its current stream.  With `stream` (a torch.cuda.Stream of that device
 or a HIP stream handle, 0 the null stream) they do as under ``torch.cuda.stream(stream)``: what they allocate
 belongs to that stream too.  Nothing synchronises: the split sizes stay in device memory, where
-`_native.DeviceGroups` takes them, so a captured graph follows the routing.  An output must not be one of
-the call's inputs.
+`_native.DeviceGroups` takes them, so a captured graph follows the routing.  An output must not be or overlap
+another tensor of the call.
 
 A slot is one (token, choice) pair, numbered token * topk + choice; a slot without an expert has expert -1
 and row -1.
