@@ -264,9 +264,12 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteArgs a, const T* __
 // expert plus those with the same expert and a smaller number; slots without an expert get -1.  The
 // result is fixed by the indices alone.  Two launches of 4.7 and 5.0 us at 32768 slots.
 
-// Slots per histogram block: at most 128 blocks up to 524288 slots, so that a block's sum over the
-// blocks before it stays short.
+// Slots per histogram block: at most SORT_BLOCKS blocks up to 524288 slots, so that a block's sum over the blocks before
+// it stays short.  Beyond that every block would read the counts of all (a square of the slots: 4096 blocks x 4 MB at
+// 16.8 M slots and 256 experts), and a launch between the two turns the counts into sums once.  256 experts, replayed
+// from a graph: 524288 slots 17.4 us in two launches, 524296 15.0 in three; 8.4 M 45 us, 67 M 273 us.
 __host__ __device__ inline int sort_chunk(int64_t slots) { return slots <= 131072 ? 1024 : 4096; }
+constexpr int64_t SORT_BLOCKS = 128;
 
 // Up to this many slots the dispatch is one launch whose workgroups each look at all of them.  Replayed from a
 // graph, 4096 wide: 8 tokens x top 2 3.0 us (6.8 in the three launches of the general form), 64 x 4 4.3 (7.8),
@@ -311,7 +314,33 @@ __device__ __forceinline__ int block_exclusive(int v, int32_t* lds) {
   return s - v;
 }
 
-template <int CHUNK>
+// The counts [blocks x experts] replaced, per expert, by the sums of the blocks before; their totals in one row more.
+// A workgroup has 16 experts (whole 64-byte pieces of the rows) and splits the blocks into 64 runs of consecutive ones.
+constexpr int SCAN_RUNS = 64;
+__global__ __launch_bounds__(1024) void sort_scan_kernel(int blocks, int experts, int32_t* __restrict__ counts) {
+  __shared__ int32_t part[SCAN_RUNS][16];
+  const int l = threadIdx.x & 15, run = threadIdx.x >> 4, e = 16 * blockIdx.x + l;
+  const int per = (blocks + SCAN_RUNS - 1) / SCAN_RUNS;
+  const int b0 = min(run * per, blocks), b1 = e < experts ? min(b0 + per, blocks) : b0;
+  int32_t* at = counts + (int64_t)b0 * experts + e;
+  int sum = 0;
+#pragma unroll 8
+  for (int i = 0; i < b1 - b0; ++i) sum += at[(int64_t)i * experts];
+  part[run][l] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int r = 0; r < run; ++r) before += part[r][l];
+#pragma unroll 8
+  for (int i = 0; i < b1 - b0; ++i) {
+    const int v = at[(int64_t)i * experts];
+    at[(int64_t)i * experts] = before;
+    before += v;
+  }
+  if (run == SCAN_RUNS - 1 && e < experts) counts[(int64_t)blocks * experts + e] = before;
+}
+
+// SCANNED: the counts are sort_scan_kernel's sums.
+template <int CHUNK, bool SCANNED>
 __global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int experts, const int32_t* __restrict__ idx,
                                                         const int32_t* __restrict__ counts,
                                                         int32_t* __restrict__ row_of_slot,
@@ -328,11 +357,16 @@ __global__ __launch_bounds__(256) void sort_rows_kernel(int64_t slots, int exper
   int before = 0, total = 0;
   if (t < experts) {
     const int nb = gridDim.x;
+    if constexpr (SCANNED) {
+      before = counts[(int64_t)blockIdx.x * experts + t];
+      total = counts[(int64_t)nb * experts + t];
+    } else {
 #pragma unroll 8
-    for (int b = 0; b < nb; ++b) {
-      const int v = counts[(int64_t)b * experts + t];
-      before += b < (int)blockIdx.x ? v : 0;
-      total += v;
+      for (int b = 0; b < nb; ++b) {
+        const int v = counts[(int64_t)b * experts + t];
+        before += b < (int)blockIdx.x ? v : 0;
+        total += v;
+      }
     }
     if (blockIdx.x == 0) splits[t] = total;
   }
@@ -853,10 +887,10 @@ int64_t mgs_moe_dispatch_workspace_bytes(int64_t tokens, int32_t topk, int32_t e
   if (experts < 1 || experts > MGS_MAX_GROUPS)
     return fail(MGS_ERR_INVALID_ARG, "num_experts %d outside [1, %d]", experts, MGS_MAX_GROUPS);
   if (tokens < 0 || tokens > INT32_MAX / topk) return fail(MGS_ERR_SHAPE, "tokens %lld: tokens x topk must be in [0, 2^31)", (long long)tokens);
-  const int64_t slots = tokens * topk, chunk = sort_chunk(slots);
+  const int64_t slots = tokens * topk, chunk = sort_chunk(slots), blocks = (slots + chunk - 1) / chunk;
   ok();
   if (slots <= SMALL_SLOTS) return 0;
-  return 4 * std::max<int64_t>(1, (slots + chunk - 1) / chunk) * experts;
+  return 4 * (blocks + (blocks > SORT_BLOCKS ? 1 : 0)) * experts;
 }
 
 int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_t* expert_idx, int64_t hidden,
@@ -908,14 +942,19 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
     return launched();
   }
   int32_t* counts = static_cast<int32_t*>(workspace);
-  auto sort = [&](auto c) {
+  auto sort = [&](auto c, auto scanned) {
     constexpr int CHUNK = decltype(c)::value;
+    constexpr bool SCANNED = decltype(scanned)::value;
     const dim3 grid((unsigned)((slots + CHUNK - 1) / CHUNK));
     hipLaunchKernelGGL(sort_count_kernel<CHUNK>, grid, dim3(256), 0, st, slots, experts, expert_idx, counts);
-    hipLaunchKernelGGL(sort_rows_kernel<CHUNK>, grid, dim3(256), 0, st, slots, experts, expert_idx, counts, row_of_slot, split_sizes);
+    if (SCANNED)
+      hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)((experts + 15) / 16)), dim3(1024), 0, st, (int)grid.x, experts, counts);
+    hipLaunchKernelGGL((sort_rows_kernel<CHUNK, SCANNED>), grid, dim3(256), 0, st, slots, experts, expert_idx, counts, row_of_slot, split_sizes);
   };
-  if (sort_chunk(slots) == 1024) sort(std::integral_constant<int, 1024>{});
-  else sort(std::integral_constant<int, 4096>{});
+  // (chunks of 1024 slots: at most 128 blocks)
+  if (sort_chunk(slots) == 1024) sort(std::integral_constant<int, 1024>{}, std::false_type{});
+  else if (slots <= SORT_BLOCKS * 4096) sort(std::integral_constant<int, 4096>{}, std::false_type{});
+  else sort(std::integral_constant<int, 4096>{}, std::true_type{});
   if (x) {
     with_unit(dtype, wide, [&](auto e, auto n) {
       typedef decltype(e) T;
