@@ -265,7 +265,8 @@ class MoELayer:
     weights' gradient.  backward(dy) returns the MLP's gradients plus `dx` and `dlogits` (the latter with the
     MLP's grad_probs); with the MLP's delay_wgrad its backward_dw() is still to be called.
     Row buffers are allocated for each step, tokens * topk rows each, so that a captured step keeps its
-    own; rows behind the last used one are neither read nor written.
+    own; rows behind the last used one are neither read nor written.  Without tokens (x [0, hidden]) the outputs
+    are empty and the weights' gradients zeros.
     """
 
     def __init__(self, mlp, topk, score="softmax", renormalize=True, scale=1.0):
@@ -278,9 +279,7 @@ class MoELayer:
         _check("x", x, (torch.bfloat16,), 2, contiguous=False)
         _check("x", x, (torch.bfloat16,), 2, contiguous=False, shape=(x.shape[0], self.mlp.h))
         _check("logits", logits, _FLOATS, 2, x.device, contiguous=False, shape=(x.shape[0], self.mlp.e))
-        if x.shape[0] == 0:
-            _fail("x has no tokens")
-        cap = x.shape[0] * self.topk
+        cap = max(x.shape[0] * self.topk, 1)  # (without tokens: buffers of one row that nothing uses)
         with torch.cuda.device(x.device):
             idx, w = moe_route(logits, self.topk, **self.route)
             rows = torch.empty((cap, self.mlp.h), dtype=torch.bfloat16, device=x.device)
@@ -296,7 +295,7 @@ class MoELayer:
                 y_rows = self.mlp.forward(rows, probs, groups)
                 y = moe_combine(row, y_rows, weights=w)
                 ctx.update(w=w, y_rows=y_rows if self.mlp.grad_probs else None)
-        self.ctx = dict(ctx, row=row)
+        self.ctx = dict(ctx, row=row, cap=cap)
         return y
 
     def backward(self, dy):
@@ -308,7 +307,7 @@ class MoELayer:
         _check("dy", dy, (torch.bfloat16,), 2, row.device, contiguous=False, shape=(row.shape[0], self.mlp.h))
         self.ctx = None
         with torch.cuda.device(dy.device):
-            drows = torch.empty((row.numel(), self.mlp.h), dtype=torch.bfloat16, device=dy.device)
+            drows = torch.empty((c["cap"], self.mlp.h), dtype=torch.bfloat16, device=dy.device)
             if "w" in c:  # the combine's weights
                 dw = moe_combine_bwd(row, dy, drows, rows=c["y_rows"], weights=c["w"])
             else:

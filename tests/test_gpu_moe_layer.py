@@ -232,3 +232,31 @@ def test_gradients_not_asked_for(M, bias):
     for g in got[1:]:
         assert all(torch.equal(v, full[k]) for k, v in g.items())
     assert "dlogits" in no_x and "dlogits" in only_p and "dx" in no_p
+
+
+@pytest.mark.parametrize("grad_x1", [False, True])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp8", "nvfp4", "mxfp4"])
+def test_no_tokens(M, fmt, bias, grad_x1):
+    """A batch without tokens (one rank's share, say): empty outputs, and weight and bias gradients of zeros; the next
+    batch is as if it had not been."""
+    import torch
+    layer = _exact_layer(M, fmt, bias, 13, grad_x1=grad_x1)[0]
+    x, logits, dy = _data(np.random.default_rng(14), True)
+    x, logits, dy = _dev16(x), to_dev(logits), _dev16(dy)
+
+    def step(n):
+        y = layer.forward(x[:n], logits[:n])
+        return dict(layer.backward(dy[:n]), y=y)
+
+    want = {k: v.clone() for k, v in step(T).items()}
+    g = step(0)
+    torch.cuda.synchronize()
+    assert g["y"].shape == (0, H) and g["dlogits"].shape == (0, E) and ("dx" in g) == grad_x1
+    if grad_x1:
+        assert g["dx"].shape == (0, H)
+    for k in ("dw1", "dw2", "db1") + (("db2",) if bias else ()):
+        assert g[k].shape == want[k].shape and not bool(g[k].any()), k
+    again = step(T)
+    torch.cuda.synchronize()
+    assert all(torch.equal(again[k], v) for k, v in want.items())
