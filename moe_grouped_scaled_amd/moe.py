@@ -279,6 +279,9 @@ class MoELayer:
         _check("x", x, (torch.bfloat16,), 2, contiguous=False)
         _check("x", x, (torch.bfloat16,), 2, contiguous=False, shape=(x.shape[0], self.mlp.h))
         _check("logits", logits, _FLOATS, 2, x.device, contiguous=False, shape=(x.shape[0], self.mlp.e))
+        for t in (self.mlp.w1, self.mlp.w2, self.mlp.b1, self.mlp.b2):
+            if t is not None and t.device != x.device:
+                _fail("x is on %s, the expert MLP's parameters are on %s", x.device, t.device)
         cap = max(x.shape[0] * self.topk, 1)  # (without tokens: buffers of one row that nothing uses)
         with torch.cuda.device(x.device):
             idx, w = moe_route(logits, self.topk, **self.route)

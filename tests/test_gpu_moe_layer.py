@@ -260,3 +260,12 @@ def test_no_tokens(M, fmt, bias, grad_x1):
     again = step(T)
     torch.cuda.synchronize()
     assert all(torch.equal(again[k], v) for k, v in want.items())
+
+
+@pytest.mark.parametrize("name", ["w1", "w2", "b1", "b2"])
+def test_parameters_on_another_device_are_refused(M, name):
+    layer = _exact_layer(M, "mxfp8", True, 15)[0]
+    x, logits, _ = _data(np.random.default_rng(16), False)
+    setattr(layer.mlp, name, getattr(layer.mlp, name).cpu())
+    with pytest.raises(ValueError, match="parameters are on cpu"):
+        layer.forward(_dev16(x), to_dev(logits))
