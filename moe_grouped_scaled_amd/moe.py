@@ -266,7 +266,8 @@ class MoELayer:
     MLP's grad_probs); with the MLP's delay_wgrad its backward_dw() is still to be called.
     Row buffers are allocated for each step, tokens * topk rows each, so that a captured step keeps its
     own; rows behind the last used one are neither read nor written.  Without tokens (x [0, hidden]) the outputs
-    are empty and the weights' gradients zeros.
+    are empty and the weights' gradients zeros.  The MLP keeps one forward's tensors at a time, so layers that
+    share one alternate forward and backward; a backward whose forward it no longer holds is refused.
     """
 
     def __init__(self, mlp, topk, score="softmax", renormalize=True, scale=1.0):
@@ -298,7 +299,9 @@ class MoELayer:
                 y_rows = self.mlp.forward(rows, probs, groups)
                 y = moe_combine(row, y_rows, weights=w)
                 ctx.update(w=w, y_rows=y_rows if self.mlp.grad_probs else None)
-        self.ctx = dict(ctx, row=row, cap=cap)
+        # (a mark in what the MLP saved, not a reference to it: that is the MLP's to free)
+        mark = self.mlp.ctx["owner"] = object()
+        self.ctx = dict(ctx, row=row, cap=cap, mark=mark)
         return y
 
     def backward(self, dy):
@@ -308,6 +311,9 @@ class MoELayer:
             _fail("backward() without a forward")
         row = c["row"]
         _check("dy", dy, (torch.bfloat16,), 2, row.device, contiguous=False, shape=(row.shape[0], self.mlp.h))
+        if (self.mlp.ctx or {}).get("owner") is not c["mark"]:
+            self.ctx = None
+            _fail("the expert MLP has run another forward or its backward since: what this one saved is gone")
         self.ctx = None
         with torch.cuda.device(dy.device):
             drows = torch.empty((c["cap"], self.mlp.h), dtype=torch.bfloat16, device=dy.device)

@@ -269,3 +269,29 @@ def test_parameters_on_another_device_are_refused(M, name):
     setattr(layer.mlp, name, getattr(layer.mlp, name).cpu())
     with pytest.raises(ValueError, match="parameters are on cpu"):
         layer.forward(_dev16(x), to_dev(logits))
+
+
+def test_layers_that_share_an_mlp(M):
+    """One MLP keeps one forward's tensors: a backward of an earlier one is refused (it would multiply with the later
+    one's), and steps that alternate are each layer's own."""
+    import torch
+    first = _exact_layer(M, "mxfp8", False, 17)[0]
+    second = M.MoELayer(first.mlp, 1, score="sigmoid")
+    rng = np.random.default_rng(18)
+    batches = [[_dev16(x), to_dev(logits), _dev16(dy)] for x, logits, dy in (_data(rng, True), _data(rng, False))]
+
+    def step(layer, b):
+        y = layer.forward(b[0], b[1])
+        return dict(layer.backward(b[2]), y=y)
+
+    want = [step(layer, b) for layer, b in zip((first, second), batches)]
+    first.forward(*batches[0][:2])
+    second.forward(*batches[1][:2])
+    with pytest.raises(ValueError, match="another forward"):
+        first.backward(batches[0][2])
+    got = second.backward(batches[1][2])
+    assert all(torch.equal(got[k], want[1][k]) for k in got)
+    with pytest.raises(ValueError, match="without a forward"):
+        first.backward(batches[0][2])
+    got = step(first, batches[0])
+    assert all(torch.equal(got[k], want[0][k]) for k in got)
