@@ -75,6 +75,12 @@ def _on_stream(stream, t, fn, *args):
         return fn(*args)
 
 
+def _int32(what, n):
+    """(The binding passes 32-bit arguments on without their upper bits; the library checks the rest.)"""
+    if n >> 31:
+        _fail("%s = %d is out of range", what, n)
+
+
 _FLOATS = (torch.bfloat16, torch.float32)
 _I32, _I64, _F32 = (torch.int32,), (torch.int64,), (torch.float32,)
 
@@ -92,6 +98,7 @@ def moe_route(logits, topk, score="softmax", renormalize=True, scale=1.0, expert
     (expert_idx int32, weights FP32), both [tokens, topk]."""
     if stream is not None:
         return _on_stream(stream, logits, moe_route, logits, topk, score, renormalize, scale, expert_idx, weights)
+    _int32("topk", topk)
     _check("logits", logits, _FLOATS, 2, contiguous=False)
     t, e = logits.shape
     dev = logits.device
@@ -130,6 +137,8 @@ def moe_route_bwd(logits, expert_idx, dweights, score="softmax", renormalize=Tru
 
 
 def moe_dispatch_workspace_bytes(tokens, topk, num_experts):
+    _int32("topk", topk)
+    _int32("num_experts", num_experts)
     n = N.LIB.mgs_moe_dispatch_workspace_bytes(tokens, topk, num_experts)
     if n < 0:
         N._check(int(n))
@@ -146,6 +155,7 @@ def moe_dispatch(expert_idx, num_experts, x=None, rows=None, weights=None, row_w
     if stream is not None:
         return _on_stream(stream, expert_idx, moe_dispatch, expert_idx, num_experts, x, rows, weights, row_weights, row_of_slot, split_sizes,
                           workspace)
+    _int32("num_experts", num_experts)
     _check("expert_idx", expert_idx, _I32, 2)
     t, k = expert_idx.shape
     dev = expert_idx.device
