@@ -42,7 +42,7 @@ class ActParams(ctypes.Structure):
 
 
 class Groups(ctypes.Structure):
-    _fields_ = [("num_groups", ctypes.c_int32), ("split_sizes", ctypes.c_void_p),
+    _fields_ = [("num_groups", ctypes.c_int32), ("split_sizes", ctypes.POINTER(ctypes.c_int64)),
                 ("max_rows", ctypes.c_int64), ("dev_table", ctypes.c_void_p)]
 
 
@@ -158,10 +158,12 @@ class _GroupsArg:
             self.struct = Groups(split_sizes.num_groups, None, split_sizes.max_rows, split_sizes.table.data_ptr())
         elif type(split_sizes) is list and all(type(m) is int for m in split_sizes):
             self.arr = array.array("q", split_sizes)
-            self.struct = Groups(len(split_sizes), self.arr.buffer_info()[0], 0, None)
+            self.struct = Groups(len(split_sizes), None, 0, None)
+            # (the address written in place: half the time of a typed pointer made for it)
+            ctypes.c_void_p.from_buffer(self.struct, Groups.split_sizes.offset).value = self.arr.buffer_info()[0]
         else:
             self.arr = np.ascontiguousarray(np.asarray(split_sizes, dtype=np.int64))
-            self.struct = Groups(len(self.arr), self.arr.ctypes.data, 0, None)
+            self.struct = Groups(len(self.arr), self.arr.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), 0, None)
         self.ref = ctypes.byref(self.struct)
 
 
