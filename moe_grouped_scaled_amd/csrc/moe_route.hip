@@ -8,6 +8,7 @@
 //
 // A slot is one (token, choice) pair, numbered token * topk + choice.
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <type_traits>
 
@@ -787,7 +788,7 @@ int check_route(const mgs_route_params* rp, int64_t tokens, int32_t experts, int
   if (!rp) return fail(MGS_ERR_INVALID_ARG, "route params are NULL");
   if (rp->score != MGS_SCORE_SOFTMAX && rp->score != MGS_SCORE_SIGMOID)
     return fail(MGS_ERR_INVALID_ARG, "unknown score function %d", rp->score);
-  if (!(rp->scale > -3.4e38f && rp->scale < 3.4e38f)) return fail(MGS_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(rp->scale)) return fail(MGS_ERR_INVALID_ARG, "scale must be finite");
   if (experts < 1 || experts > MGS_MAX_GROUPS)
     return fail(MGS_ERR_INVALID_ARG, "num_experts %d outside [1, %d]", experts, MGS_MAX_GROUPS);
   if (topk < 1 || topk > MGS_MAX_TOPK || topk > experts)
