@@ -521,7 +521,7 @@ __global__ __launch_bounds__(256) void scatter_kernel(MoveArgs a, const int32_t*
 
 // The whole dispatch in one launch, for few slots: a workgroup per token counts, over all slots, those that
 // precede each of its own in the sorted order, then copies its row.  Workgroup 0 also takes the split sizes.
-template <typename T, int V, int KMAX, bool NT>
+template <typename T, int V, int KMAX>
 __global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slots, const int32_t* __restrict__ idx,
                                                              const T* __restrict__ x, const float* __restrict__ weights,
                                                              T* __restrict__ rows, float* __restrict__ row_weights,
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(256) void dispatch_small_kernel(MoveArgs a, int slo
       if (row_weights && r[c] >= 0) row_weights[r[c]] = weights[slot0 + c];
     }
   }
-  if (rows) scatter_row<T, V, KMAX, NT>(a, r, x + t * a.ld, rows, tid, 256);
+  if (rows) scatter_row<T, V, KMAX, false>(a, r, x + t * a.ld, rows, tid, 256);
 }
 
 // y of every token: the sum over its slots' rows in slot order, in FP32, with weights if given.  Row numbers
@@ -935,7 +935,7 @@ int mgs_moe_dispatch(int64_t tokens, int32_t topk, int32_t experts, const int32_
     with_unit(dtype, wide, [&](auto e, auto n) {
       typedef decltype(e) T;
       with_topk(topk, [&](auto k) {
-        hipLaunchKernelGGL((dispatch_small_kernel<T, decltype(n)::value, decltype(k)::value, false>), dim3((unsigned)std::max<int64_t>(1, tokens)),
+        hipLaunchKernelGGL((dispatch_small_kernel<T, decltype(n)::value, decltype(k)::value>), dim3((unsigned)std::max<int64_t>(1, tokens)),
                            dim3(256), 0, st, a, (int)slots, expert_idx, static_cast<const T*>(x), weights,
                            static_cast<T*>(tokens ? rows : nullptr), row_weights, row_of_slot, split_sizes);
       });
