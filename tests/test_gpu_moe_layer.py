@@ -295,3 +295,41 @@ def test_layers_that_share_an_mlp(M):
         first.backward(batches[0][2])
     got = step(first, batches[0])
     assert all(torch.equal(got[k], want[0][k]) for k in got)
+
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_one_graph_follows_the_routing(M, fmt, bias):
+    """One captured step replayed for other routings, eager steps and synchronizations between the replays; in the last
+    one no token has an expert."""
+    import torch
+    layer = _exact_layer(M, fmt, bias, 19)[0]
+    rng = np.random.default_rng(20)
+    batches = [[_dev16(x), to_dev(logits), _dev16(dy)] for x, logits, dy in (_data(rng, i != 1) for i in range(4))]
+    batches[3][1].fill_(-float("inf"))
+
+    def step(b):
+        y = layer.forward(b[0], b[1])
+        return dict(layer.backward(b[2]), y=y)
+
+    held = [t.clone() for t in batches[0]]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(held)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(held)
+    for i in (0, 1, 3, 2, 0):
+        want = {k: v.clone() for k, v in step(batches[i]).items()}
+        torch.cuda.synchronize()
+        for dst, src in zip(held, batches[i]):
+            dst.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        for k, v in want.items():
+            assert torch.equal(out[k], v), (i, k)
+        if i == 3:
+            assert not any(bool(v.any()) for v in want.values())
