@@ -1205,15 +1205,16 @@ int64_t count_tiles(const GemmArgs& ga, const GroupTable& gt, int tm, int tn) {
 }
 
 // MXFP4: which kernel and tile.  The 256 x 256 kernel needs groups of more than 64 rows and work for the chip:
-// below 1024 tiles of 64 x 64 a tile's own time (27 us at K = 4096) stands alone.  4096 x 4096, one expert x
-// 256, 1024, 2048 rows: 28.1, 29.6, 30.6 us with it and 9.1, 22.8, 41.1 us with the few-rows kernel; 8 experts
-// x 128, 256 rows 30.2, 30.3 and 25.3, 40.9 us; 16 experts x 64, 96 rows 36.4, 37.3 and 32.2, 44.9 us.  The few-rows
-// kernel takes the largest tile that still gives two workgroups per CU: 64 x 64 reads the weights once
-// for 64 rows, smaller ones fill the chip (one expert x 64 rows: 9.9 us in 64 x 64, 6.1 us in 32 x 32), and
-// no taller tile than the largest group needs (16 experts x 2 rows: 30.8 us with 16 x 32, 35.9 with 64 x 64).
-// Its ring holds two units where there are few workgroups (one expert x 1 row, 8192 x 8192: 8.8 against 10.2
+// below 1024 tiles of 64 x 64 a tile's own time (29 us at K = 4096) stands alone.  n = k = 4096, one expert x 256, 1024,
+// 2048 rows: 29.1, 30.0, 32.6 us with it and 10.6, 23.7, 43.6 us on 64 x 64 tiles; 8 experts x 128, 256 rows 30.6, 30.3
+// and 26.0, 48.5 us; 16 experts x 64, 96 rows 49.9, 47.5 and 43.2, 57.3 us.  The border hardly moves with K (both
+// kernels' times follow it): one expert x 1024, 2048 rows at K = 512 11.5, 11.5 and 12.6, 22.0 us, at K = 16384 92, 92 and
+// 65, 120 us.  The few-rows kernel takes the largest tile that still gives two workgroups per CU: 64 x 64 reads the
+// weights once for 64 rows, smaller ones fill the chip (one expert x 64 rows: 8.4 us in 64 x 64, 5.2 us in 32 x 32), and
+// no taller tile than the largest group needs (16 experts x 2 rows: 30.9 us with 16 x 32, 35.8 with 64 x 64).
+// Its ring holds two units where there are few workgroups (one expert x 1 row, 8192 x 8192: 8.8 against 10.1
 // us with one), one where several workgroups per CU hide each other's loads (32 experts x 1 row, 7168 x
-// 2048: 45.8 against 56.4 us with two).  With device-resident split sizes the host knows the capacity only:
+// 2048: 45.1 against 55.7 us with two).  With device-resident split sizes the host knows the capacity only:
 // the largest group is taken to have twice the mean, and any other routing is right, if slower.
 GemmVariant mxfp4_variant(const GemmArgs& ga, const GroupTable& gt) {
   int64_t most = 0;

@@ -181,11 +181,14 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_rows_kernel(GemmArgs ga, GemmT
 // the MFMAs of that substep the next step's first fragments are read and the loads of the step after it
 // begin, so neither the LDS reads nor the barrier leave the matrix cores without work.
 //
-// What bounds it: 8192^3 with random codes takes 255-283 us (4.3-3.9 PFLOP/s), the same launch with every code
-// equal 195 us (5.6): under random data the card lowers its clock (1.73 GHz, counted), at which the MFMAs alone are
-// 57% of the cycles; a tile's start and end are most of the rest (16 x 2048 x 4096 x 4096: 288 against 235 us).  Two
-// workgroups per CU on 128 x 256 tiles, whose starts and ends overlap, need 1.5 times the operand loads per product
-// and took 321 us where this kernel took 267 (8192^3).
+// What bounds it, in cycles of a CU (counted): 8192^3 takes 444,000 whatever the codes, of which the MFMAs are 262,000
+// (2048 of a K step, 59%).  16 x 2048 x 4096 x 4096, the same K steps in eight tiles a CU instead of four, takes
+// 514,000: a tile's start and end cost 17,600 cycles, 16% of 8192^3 and 27% of it.  The rest, 25%, is inside the K
+// loop, 870 cycles of a step: its 68 KiB then come at 24 bytes per cycle and CU, and a kernel that only loads tiles in
+// this order reached 21.  The time is those cycles at the clock the data leave: 208-213 us with every code equal
+// (2.25 GHz), 258-299 us with random codes (1.8 GHz and less, lowest on a card that has been busy longer).
+// Two workgroups per CU on 128 x 256 tiles, whose starts and ends overlap, need 1.5 times the operand loads per product
+// and took 321 us where this kernel took 267 in the same run (8192^3).
 constexpr int F4_KSTEP = 256;
 constexpr int F4_ROWB = F4_KSTEP / 2;
 constexpr int F4_DATA = BM2 * F4_ROWB;              // per operand and stage
@@ -213,8 +216,10 @@ __device__ __forceinline__ void mfma_scale_fp4(v16f& acc, const v4i& b, const v4
 // 128 wm + 32 fm + r32 and the four columns 128 wn + 32 fn + 8 g + 4 h32 .. + 3.  Stored from there, an
 // instruction would write 32 bytes of each of 32 rows; 32 rows at a time go through the wave's part of LDS
 // instead (free by then) and leave it as whole 256-byte (FP32: 512-byte) row pieces, non-temporal: the
-// outputs of the tiles in flight fill the L2, and the operands are read again.  16 x 2048 x 4096 x 4096: 288 us
-// (331 from the fragments, 317 through LDS with plain stores); its weight gradient in FP32 407 us (560, 470).
+// outputs of the tiles in flight fill the L2, and the operands are read again.  16 x 2048 x 4096 x 4096, in one run:
+// 288 us (331 from the fragments, 317 through LDS with plain stores); its weight gradient in FP32 407 us (560, 470).
+// (The same launches in a traced run of 40 in a row: 332 us at the median, 302 at least; the gradient 435 and 408,
+// accumulating 637 and 602.)
 template <bool F32>
 __device__ __forceinline__ void epilogue_fp4(const TileJob& j, v16f (&acc)[4][4], const uint2* bias_lds, uint8_t* buf,
                                              bool accumulate, int wm, int wn, int lane) {

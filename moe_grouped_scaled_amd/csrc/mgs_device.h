@@ -202,7 +202,9 @@ __device__ __forceinline__ uint32_t mx4_scale_code(float amax) {
 // `amax`: the E8M0 scale code and the eight E2M1 codes in a dword (value 2i in the low nibble of byte
 // i).  The scaled convert divides by the power of two exactly, rounds to nearest-even and saturates
 // at +-6 (checked on the device for every scale code 0..254, the subnormal 2^-127 included).  Quantizing
-// 32768 x 4096 rowwise takes 62-65 us for 340 MB, the rate of a large copy.
+// 32768 x 4096 rowwise takes 61-64 us for 340 MB, the rate of a large copy; SReLU before it 68 us, with the columnwise
+// copy too 90 us for 411 MB; the SReLU backward with both copies of dx, dprobs and the regenerated columnwise copy of the
+// activation 183 us for 751 MB.
 struct Mx4 {
   uint32_t code, q;
 };

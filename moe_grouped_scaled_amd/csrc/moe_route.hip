@@ -29,7 +29,8 @@ namespace {
 // the next key, agree in the other 24 bits picks again with whole keys.
 //
 // Bound by the picks (VALU): 65536 tokens x 256 FP32 experts, top 8, takes 23 us for 67 MB of logits (13 us at
-// the rate of a large copy); 16 tokens x 32 experts 2.0 us, the shortest a launch is here.
+// the rate of a large copy): 678 VALU instructions a wave, whose issue fills the cycles that a CU is busy (counted).
+// 16 tokens x 32 experts 2.0 us, the shortest a launch is here.
 constexpr int ROUTE_LANES = 16;
 constexpr int DPP_ROW_ROR1 = 0x121, DPP_ROW_ROR2 = 0x122;
 
@@ -486,8 +487,8 @@ __device__ __forceinline__ int slot_row(const MoveArgs& a, const int32_t* __rest
   return r >= 0 && r < a.num_rows ? r : -1;
 }
 
-// x row of every token into the rows of its slots (the token's unit is read once).  Bound by bytes: 76 us for
-// 403 MB (16384 tokens x 4096, top 2: 5.3 TB/s, mostly writes).
+// x row of every token into the rows of its slots (the token's unit is read once).  Bound by bytes: 74 us for
+// 403 MB (16384 tokens x 4096, top 2: 5.4 TB/s, mostly writes).
 template <typename T, int V, int KMAX, bool NT>
 __device__ __forceinline__ void scatter_row(const MoveArgs& a, const int (&r)[KMAX], const T* __restrict__ x,
                                             T* __restrict__ rows, int u, int tpt) {
@@ -617,7 +618,8 @@ __global__ __launch_bounds__(256) void combine_kernel(MoveArgs a, const int32_t*
 }
 
 // d(rows) = w dy and d(w) = <dy, rows>, four slots of a token at a time: a unit of dy is read once for them.
-// The sums run over the token's threads by lane exchanges, then over its waves in order.  10 us for 1021 tokens x
+// The sums run over the token's threads by lane exchanges, then over its waves in order.  Bound by bytes: 114 us for
+// 671 MB (16384 tokens x 4096 BF16, top 2: 5.9 TB/s), 369 us for 2.0 GB (8192 x 7168, top 8).  10 us for 1021 tokens x
 // 1001 FP32, top 3 (23 MB): single elements, four dependent passes a row; with the passes' loads ahead of their
 // sums it took 9.5.
 template <typename T, int V, bool NT>
