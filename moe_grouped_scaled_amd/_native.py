@@ -159,7 +159,7 @@ class _GroupsArg:
         elif type(split_sizes) is list and all(type(m) is int for m in split_sizes):
             self.arr = array.array("q", split_sizes)
             self.struct = Groups(len(split_sizes), None, 0, None)
-            # (the address written in place: half the time of a typed pointer made for it)
+            # (the address written in place: 0.5 us less than making a typed pointer of it)
             ctypes.c_void_p.from_buffer(self.struct, Groups.split_sizes.offset).value = self.arr.buffer_info()[0]
         else:
             self.arr = np.ascontiguousarray(np.asarray(split_sizes, dtype=np.int64))

@@ -757,6 +757,7 @@ struct Span {
 Span span(const char* name, const void* p, int64_t bytes) { return {name, p, p ? bytes : 0}; }
 Span span_rows(const char* name, const void* p, int64_t rows, int64_t width, int64_t ld, int dtype) {
   const int64_t es = dtype == MGS_DTYPE_BF16 ? 2 : 4;
+  if (!p) return span(name, p, 0);  // (its width was not checked)
   return span(name, p, (ld == width ? rows : std::min<int64_t>(rows, 1)) * width * es);
 }
 
