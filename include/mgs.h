@@ -424,6 +424,48 @@ int mgs_moe_combine_bwd(int64_t tokens, int32_t topk, int64_t hidden, int32_t dt
                         const int32_t* row_of_slot, int64_t num_rows, const void* dy, int64_t lddy,
                         const void* rows, const float* weights, void* drows, float* dweights, void* stream);
 
+/* ---- The expert block without quantization --------------------------------------------------------
+ * [P2] sequence diagram: the same grouped calls (FC1, gated activation with the row's scale, FC2, and back) on
+ * BF16 operands as they lie in memory, for a layer that is trained in BF16.  Group conventions as above (host or
+ * device-resident split sizes; rows past the last used one are neither read nor written).  Widths are multiples
+ * of 8 up to 2^20; BF16 and FP32 tensors start on 16-byte boundaries (probs, dprobs and the workspace: 4).  No
+ * output may be or overlap another tensor of its call.  Products accumulate in FP32; results are deterministic. */
+
+/* Grouped product of BF16 tensors:
+ *   FPROP   C [M x n] = A_g B_g^T    a [M x k], b [E x n x k]; bias_bf16 [E x n] nullable
+ *   DGRAD   C [M x n] = A_g B_g      a [M x k], b [E x k x n] (the forward's weight as it is stored); bias as above
+ *   WGRAD   C_g [m x n] = A_g^T B_g  a [M x m], b [M x n], k = M, c [E x m x n] (an empty group writes zeros, or leaves
+ *                                    C unchanged if accumulating)
+ *   c_dtype BF16 (one rounding) or F32; accumulate != 0 adds into C (F32 only). */
+int mgs_grouped_gemm_bf16(int32_t mode, const mgs_groups* groups, int64_t m, int64_t n, int64_t k, const void* a_bf16,
+                          const void* b_bf16, void* c, int32_t c_dtype, const void* bias_bf16, int32_t accumulate,
+                          void* stream);
+
+/* Forward of the gated block in one kernel: with [gate | up] = x_g W_g^T + bias in FP32,
+ *   h = act(gate, up) * probs[row], rounded to BF16 once.
+ *   act      a gated kind (SWIGLU, CLAMPED_SWIGLU, GLU)
+ *   x_bf16   [M x k]; w_bf16 [E x 2f x k]; bias_bf16 [E x 2f] nullable; probs [M] FP32, NULL means 1
+ *   h_bf16   [M x f]
+ *   pre_bf16 [M x 2f] nullable: [gate | up] rounded to BF16, which the backward takes (CLAMPED_SWIGLU: to the nearest
+ *            value on the same side of the clamps, where the derivative jumps) */
+int mgs_grouped_gated_fwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t k, const void* x_bf16,
+                          const void* w_bf16, const void* bias_bf16, const float* probs, void* h_bf16, void* pre_bf16,
+                          void* stream);
+
+/* Backward of the second linear and the activation in one kernel: with da = dy_g W2_g in FP32,
+ *   dpre = da * probs[row] * (d act / d gate, d act / d up) at pre, dprobs[row] = sum_j da * act(pre).
+ *   dy_bf16 [M x n]; w2_bf16 [E x n x f]; pre_bf16 [M x 2f] of the forward; probs as in the forward
+ *   dpre_bf16 [M x 2f]; the weights' and inputs' gradients are products of it (DGRAD and WGRAD above)
+ *   h_bf16   [M x f] nullable: act(pre) * probs again, the second linear's input (recompute)
+ *   dprobs   [M] FP32 nullable; needs the workspace, mgs_grouped_gated_bwd_workspace_bytes() bytes of
+ *            scratch, caller-owned, contents undefined before and after; calls sharing it must not overlap */
+int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t n, const void* dy_bf16,
+                          const void* w2_bf16, const void* pre_bf16, const float* probs, void* dpre_bf16, void* h_bf16,
+                          float* dprobs, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of mgs_grouped_gated_bwd's dprobs (negative MGS_ERR_* on invalid arguments). */
+int64_t mgs_grouped_gated_bwd_workspace_bytes(const mgs_groups* groups, int64_t f);
+
 #ifdef __cplusplus
 }
 #endif

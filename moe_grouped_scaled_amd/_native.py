@@ -94,6 +94,10 @@ def _load():
         "mgs_moe_dispatch_bwd": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, vp, vp, i64, vp, vp]),
         "mgs_moe_combine": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, vp, vp, i64, vp]),
         "mgs_moe_combine_bwd": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
+        "mgs_grouped_gemm_bf16": (ctypes.c_int, [i32, pgr, i64, i64, i64, vp, vp, vp, i32, vp, i32, vp]),
+        "mgs_grouped_gated_fwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp]),
+        "mgs_grouped_gated_bwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "mgs_grouped_gated_bwd_workspace_bytes": (i64, [pgr, i64]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -109,7 +113,9 @@ EXPORTED = ("mgs_abi_version", "mgs_last_error", "mgs_groups_table_bytes", "mgs_
             "mgs_grouped_scaled_act_bwd", "mgs_grouped_scaled_act_bwd_noalloc", "mgs_act_bwd_workspace_bytes", "mgs_grouped_mx_quantize",
             "mgs_grouped_mx_quantize_workspace_bytes", "mgs_grouped_gemm_mx", "mgs_grouped_gemm_mx_fprop_act",
             "mgs_grouped_col_sum", "mgs_moe_route", "mgs_moe_route_bwd", "mgs_moe_dispatch_workspace_bytes",
-            "mgs_moe_dispatch", "mgs_moe_dispatch_bwd", "mgs_moe_combine", "mgs_moe_combine_bwd")
+            "mgs_moe_dispatch", "mgs_moe_dispatch_bwd", "mgs_moe_combine", "mgs_moe_combine_bwd",
+            "mgs_grouped_gemm_bf16", "mgs_grouped_gated_fwd", "mgs_grouped_gated_bwd",
+            "mgs_grouped_gated_bwd_workspace_bytes")
 
 
 def _check(rc):

@@ -50,13 +50,17 @@ bool valid_fmt(int32_t fmt) { return fmt == MGS_FMT_MXFP8 || fmt == MGS_FMT_NVFP
 
 bool is_gated(int kind) { return kind == MGS_ACT_SWIGLU || kind == MGS_ACT_CLAMPED_SWIGLU || kind == MGS_ACT_GLU; }
 
+}  // namespace
+
+namespace mgs {
+
 // Byte offset of the GEMM tile table after the group table in a device table.
-constexpr int64_t kDevGemmTableOffset = (sizeof(mgs::GroupTable) + 255) / 256 * 256;
+static constexpr int64_t kDevGemmTableOffset = (sizeof(mgs::GroupTable) + 255) / 256 * 256;
 
 // Validates the groups and fills the panel table.  Returns MGS_OK or an error code.  Device-resident
 // split sizes: the table describes the layout for the row capacity (total_rows = max_rows, num_panels
 // = the padded-panel bound) and points to the device table holding the actual offsets.
-int build_groups(const mgs_groups* groups, mgs::GroupTable* gt, int64_t* total_rows) {
+int build_groups(const mgs_groups* groups, GroupTable* gt, int64_t* total_rows) {
   if (!groups) return fail(MGS_ERR_INVALID_ARG, "groups is NULL");
   if (groups->num_groups < 1 || groups->num_groups > MGS_MAX_GROUPS)
     return fail(MGS_ERR_INVALID_ARG, "num_groups %d outside [1, %d]", groups->num_groups, MGS_MAX_GROUPS);
@@ -66,12 +70,12 @@ int build_groups(const mgs_groups* groups, mgs::GroupTable* gt, int64_t* total_r
     if (!groups->dev_table)
       return fail(MGS_ERR_INVALID_ARG, "split_sizes is NULL and no dev_table for device-resident split sizes");
     const int64_t cap = groups->max_rows;
-    if (cap <= 0 || cap > INT32_MAX - 64 - (int64_t)mgs::COL_ALIGN * (groups->num_groups + 1))
+    if (cap <= 0 || cap > INT32_MAX - 64 - (int64_t)COL_ALIGN * (groups->num_groups + 1))
       return fail(MGS_ERR_SHAPE, "max_rows = %lld outside [1, 2^31 - 64 - 128 (E + 1)]", (long long)cap);
     gt->total_rows = (int32_t)cap;
-    gt->num_panels = (int32_t)(((cap + mgs::COL_ALIGN - 1) / mgs::COL_ALIGN + groups->num_groups) *
-                               (mgs::COL_ALIGN / mgs::PANEL_ROWS));
-    gt->dev = static_cast<const mgs::GroupTable*>(groups->dev_table);
+    gt->num_panels = (int32_t)(((cap + COL_ALIGN - 1) / COL_ALIGN + groups->num_groups) *
+                               (COL_ALIGN / PANEL_ROWS));
+    gt->dev = static_cast<const GroupTable*>(groups->dev_table);
     *total_rows = cap;
     return MGS_OK;
   }
@@ -82,7 +86,7 @@ int build_groups(const mgs_groups* groups, mgs::GroupTable* gt, int64_t* total_r
     gt->row_off[g] = (int32_t)rows;
     gt->panel_off[g] = (int32_t)panels;
     rows += m;
-    panels += (m + mgs::COL_ALIGN - 1) / mgs::COL_ALIGN * (mgs::COL_ALIGN / mgs::PANEL_ROWS);
+    panels += (m + COL_ALIGN - 1) / COL_ALIGN * (COL_ALIGN / PANEL_ROWS);
     if (rows > INT32_MAX - 64) return fail(MGS_ERR_SHAPE, "total rows exceed 2^31 - 64");
   }
   gt->row_off[groups->num_groups] = (int32_t)rows;
@@ -92,6 +96,20 @@ int build_groups(const mgs_groups* groups, mgs::GroupTable* gt, int64_t* total_r
   *total_rows = rows;
   return MGS_OK;
 }
+
+GemmTable* dev_gemm_table(const mgs_groups* groups) {
+  return groups->split_sizes ? nullptr
+                             : reinterpret_cast<GemmTable*>(static_cast<uint8_t*>(groups->dev_table) +
+                                                                 kDevGemmTableOffset);
+}
+
+}  // namespace mgs
+
+namespace {
+
+using mgs::build_groups;
+using mgs::dev_gemm_table;
+using mgs::kDevGemmTableOffset;
 
 int check_width(int64_t w, const char* what) {
   if (w <= 0 || w % 32 != 0)
@@ -173,13 +191,6 @@ mgs::QOut make_qout(const mgs_qbuf* row, const mgs_qbuf* col, int64_t width) {
 }
 
 bool device_splits(const mgs::GroupTable& gt) { return gt.dev != nullptr; }
-
-mgs::GemmTable* dev_gemm_table(const mgs_groups* groups) {
-  return groups->split_sizes ? nullptr
-                             : reinterpret_cast<mgs::GemmTable*>(static_cast<uint8_t*>(groups->dev_table) +
-                                                                 kDevGemmTableOffset);
-}
-
 
 // MXFP4 GEMM kernels address the scale arrays through 32-bit offsets: the rowwise scales of A (all rows)
 // and of the weights (all experts) stay below 2^31 bytes.  The columnwise operands of a weight gradient have

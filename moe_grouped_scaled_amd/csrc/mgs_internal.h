@@ -13,6 +13,13 @@ namespace mgs {
 int fail(int code, const char* fmt, ...);
 int ok();
 
+struct GroupTable;
+struct GemmTable;
+// Validates the groups and fills the table of their layout (mgs_api.hip); *total_rows: M, or the capacity.
+int build_groups(const mgs_groups* groups, GroupTable* gt, int64_t* total_rows);
+// The GEMM tile table's place in the groups' device table (NULL with host split sizes).
+GemmTable* dev_gemm_table(const mgs_groups* groups);
+
 // Rows of one panel: a panel is 32 consecutive rows of one group, the unit of the columnwise
 // quantization blocks (32 for MXFP8, 2 x 16 for NVFP4).
 constexpr int PANEL_ROWS = 32;
