@@ -466,6 +466,59 @@ int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, i
 /* Workspace bytes of mgs_grouped_gated_bwd's dprobs (negative MGS_ERR_* on invalid arguments). */
 int64_t mgs_grouped_gated_bwd_workspace_bytes(const mgs_groups* groups, int64_t f);
 
+/* ---- Weights in 4 bits with BF16 rows --------------------------------------------------------------
+ * The serving form of the block above: each weight is (q - z) s with a code q in 0 .. 15 and, per group of 32, 64 or
+ * 128 elements along k, a BF16 scale s and a zero point z in 0 .. 15 (8 where there are none).  Rows stay in BF16, sums
+ * are FP32, no weight is rounded.  Made for few rows per expert (decoding); any number is right.  x is finite: a row with
+ * an infinity or NaN gives NaN, in that row only.  n up to 2^20 of any size, k a multiple of the group up to 2^20. */
+
+/* Bytes of packed weights [experts x n x k] (negative MGS_ERR_* on invalid arguments). */
+int64_t mgs_w4_nbytes(int32_t experts, int64_t n, int64_t k, int32_t group, int32_t zeros);
+
+/* Lays weights out for the products below, once.
+ *   codes [experts x n x k / 2], two codes a byte, the even element in the low half; scales_bf16 [experts x n x k / group];
+ *   zeros [experts x n x k / group] (0 .. 15) or NULL; out mgs_w4_nbytes() bytes, 16-byte aligned */
+int mgs_w4_pack(int32_t experts, int64_t n, int64_t k, int32_t group, const uint8_t* codes, const void* scales_bf16,
+                const uint8_t* zeros, void* out, void* stream);
+
+/* Codes, scales and zero points (NULL: symmetric) of finite BF16 weights [experts x n x k], round to nearest.  With zero
+ * points the steps cover [min(w, 0), max(w, 0)] of a group in 15, without them [-amax, amax] in 14; the scale is
+ * rounded to BF16 before the codes are taken. */
+int mgs_w4_quantize(int32_t experts, int64_t n, int64_t k, int32_t group, const void* w_bf16, uint8_t* codes, void* scales_bf16,
+                    uint8_t* zeros, void* stream);
+
+/* c [M x n] = x_g w_g^T + bias: x_bf16 [M x k] and w (packed [E x n x k], `zeros` as it was packed) 16-byte aligned,
+ * bias_bf16 [E x n] nullable, c BF16 or F32.  No output may be or overlap another tensor of the call, here and below. */
+int mgs_grouped_gemm_w4(const mgs_groups* groups, int64_t n, int64_t k, int32_t group, int32_t zeros, const void* x_bf16,
+                        const void* w, const void* bias_bf16, void* c, int32_t c_dtype, void* stream);
+
+/* h [M x f] BF16 = act(gate, up) * probs[row] in one kernel, [gate | up] = x_g w_g^T + bias; w packed [E x 2f x k], f a
+ * multiple of 16 up to 2^19; act, bias_bf16 [E x 2f] and probs as in mgs_grouped_gated_fwd. */
+int mgs_grouped_gated_w4(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t k, int32_t group, int32_t zeros,
+                         const void* x_bf16, const void* w, const void* bias_bf16, const float* probs, void* h_bf16, void* stream);
+
+/* ---- Norm of the gradients ------------------------------------------------------------------------- */
+
+/* One gradient: `numel` contiguous elements, and where its scaled values go (the same address and type: in place). */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t grad_dtype, out_dtype; /* mgs_dtype */
+} mgs_grad;
+
+/* norm[0] = the square root of the sum of the squares of all elements of all gradients, summed in FP64 in a fixed order;
+ * with clip != 0 also out = grad * min(1, max_norm / (norm + eps)), one rounding to the output's type (the factor is
+ * FP32).  A NaN norm makes every output NaN, an infinite one zeros (NaN where the gradient is infinite).
+ * `grads` is a HOST array of `count`; empty gradients may be NULL.  No output may be or overlap another tensor of the
+ * call, but for a gradient scaled in place.
+ *   workspace  mgs_grad_norm_workspace_bytes() bytes, 8-byte aligned, caller-owned, contents undefined before and
+ *              after; calls sharing it must not overlap */
+int mgs_grad_norm(int32_t count, const mgs_grad* grads, float* norm, void* workspace, int64_t workspace_bytes, int32_t clip,
+                  float max_norm, float eps, void* stream);
+
+int64_t mgs_grad_norm_workspace_bytes(int32_t count, const mgs_grad* grads);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,7 +5,8 @@ block quantization + grouped MX GEMM, behind the C ABI of include/mgs.h.
 expert-MLP training step (FC1 -> scaled activation -> FC2, recompute, delayed wgrad, bias) through it;
 ``moe`` routes tokens to the experts and back (top-k router, dispatch, combine, their gradients) and holds
 ``MoELayer``, the layer from router logits to token outputs; ``gated`` has the gated expert block in BF16, forward
-and backward, without quantization (``GatedMLP``).
+and backward, without quantization (``GatedMLP``); ``w4`` serves it with 4-bit weights (``W4GatedMLP``), and
+``grad_clip`` has the norm of the gradients and their clipping.
 Importing the package loads libmgs.so and raises if it is missing: there is no fallback path.
 """
 
@@ -31,6 +32,7 @@ from .gated import (  # noqa: F401
     grouped_gated_fwd,
     grouped_gemm_bf16,
 )
+from .grad_clip import clip_grad_norm, grad_norm  # noqa: F401
 from .moe import (  # noqa: F401
     MoELayer,
     moe_combine,
@@ -39,4 +41,12 @@ from .moe import (  # noqa: F401
     moe_dispatch_bwd,
     moe_route,
     moe_route_bwd,
+)
+from .w4 import (  # noqa: F401
+    W4GatedMLP,
+    W4Tensor,
+    grouped_gated_w4,
+    grouped_gemm_w4,
+    w4_pack,
+    w4_quantize,
 )

@@ -55,6 +55,11 @@ class RouteParams(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 RHT_ON = 1 << 16  # mgs_qbuf.rht: bit 16 enables the Hadamard transform, bits 0..15 are its signs
 
 
@@ -98,6 +103,13 @@ def _load():
         "mgs_grouped_gated_fwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp]),
         "mgs_grouped_gated_bwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
         "mgs_grouped_gated_bwd_workspace_bytes": (i64, [pgr, i64]),
+        "mgs_w4_nbytes": (i64, [i32, i64, i64, i32, i32]),
+        "mgs_w4_pack": (ctypes.c_int, [i32, i64, i64, i32, vp, vp, vp, vp, vp]),
+        "mgs_w4_quantize": (ctypes.c_int, [i32, i64, i64, i32, vp, vp, vp, vp, vp]),
+        "mgs_grouped_gemm_w4": (ctypes.c_int, [pgr, i64, i64, i32, i32, vp, vp, vp, vp, i32, vp]),
+        "mgs_grouped_gated_w4": (ctypes.c_int, [pact, pgr, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]),
+        "mgs_grad_norm": (ctypes.c_int, [i32, vp, vp, vp, i64, i32, ctypes.c_float, ctypes.c_float, vp]),
+        "mgs_grad_norm_workspace_bytes": (i64, [i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -115,7 +127,8 @@ EXPORTED = ("mgs_abi_version", "mgs_last_error", "mgs_groups_table_bytes", "mgs_
             "mgs_grouped_col_sum", "mgs_moe_route", "mgs_moe_route_bwd", "mgs_moe_dispatch_workspace_bytes",
             "mgs_moe_dispatch", "mgs_moe_dispatch_bwd", "mgs_moe_combine", "mgs_moe_combine_bwd",
             "mgs_grouped_gemm_bf16", "mgs_grouped_gated_fwd", "mgs_grouped_gated_bwd",
-            "mgs_grouped_gated_bwd_workspace_bytes")
+            "mgs_grouped_gated_bwd_workspace_bytes", "mgs_w4_nbytes", "mgs_w4_pack", "mgs_w4_quantize",
+            "mgs_grouped_gemm_w4", "mgs_grouped_gated_w4", "mgs_grad_norm", "mgs_grad_norm_workspace_bytes")
 
 
 def _check(rc):

@@ -584,7 +584,7 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
   const int ntn = (int)((ga.n + TN - 1) / TN);
   const int g = blockIdx.x / ntn, tn = blockIdx.x - g * ntn;
   const GroupTable& t = gt.dev ? *gt.dev : gt;
-  const int64_t r0 = t.row_off[g], r1 = t.row_off[g + 1];
+  const int64_t r0 = __builtin_amdgcn_readfirstlane(t.row_off[g]), r1 = __builtin_amdgcn_readfirstlane(t.row_off[g + 1]);
   if (r0 == r1) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
