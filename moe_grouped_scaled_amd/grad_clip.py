@@ -5,6 +5,8 @@ return the norm as an FP32 tensor [1] on that device: nothing synchronises, and 
 replay's own norm.  The addresses of the gradients travel with the call.
 """
 
+import array
+
 import torch
 
 from . import _native as N
@@ -33,18 +35,25 @@ def _run(grads, clip, max_norm, eps, out, workspace, norm):
     if out is not None and len(out) != len(grads):
         _fail("out has %d tensors, grads has %d", len(out), len(grads))
     dev = _tensor("grads[0]", grads[0], None).device
-    table = (N.Grad * len(grads))()
+    # mgs_grad rows: address, output's address, elements, the two types in one word
+    rows, index, types, is_tensor = [], dev.index, _TYPES, torch.Tensor
     for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor) or g.dtype not in _TYPES or g.device != dev or not g.is_contiguous():
+        if not isinstance(g, is_tensor) or g.dtype not in types or g.get_device() != index or not g.is_contiguous():
             _tensor("grads[%d]" % i, g, dev)
-        o = g
-        if out is not None:
-            o = _tensor("out[%d]" % i, out[i], dev)
-            if o.shape != g.shape:
-                _fail("out[%d] has shape %s, expected %s", i, tuple(o.shape), tuple(g.shape))
-        e = table[i]
-        e.grad, e.out, e.numel, e.grad_dtype, e.out_dtype = g.data_ptr(), o.data_ptr(), g.numel(), _TYPES[g.dtype], _TYPES[o.dtype]
-    need = N.LIB.mgs_grad_norm_workspace_bytes(len(grads), table)
+        t, n = types[g.dtype], g.numel()
+        if out is None:
+            at = g.data_ptr()
+            rows += (at, at, n, t << 32 | t)
+            continue
+        o = out[i]
+        if not isinstance(o, is_tensor) or o.dtype not in types or o.get_device() != index or not o.is_contiguous():
+            _tensor("out[%d]" % i, o, dev)
+        if o.numel() != n:
+            _fail("out[%d] has %d elements, expected %d", i, o.numel(), n)
+        rows += (g.data_ptr(), o.data_ptr(), n, types[o.dtype] << 32 | t)
+    table = array.array("q", rows)
+    at = table.buffer_info()[0]
+    need = N.LIB.mgs_grad_norm_workspace_bytes(len(grads), at)
     if need < 0:
         N._check(int(need))
     if workspace is None:
@@ -55,7 +64,7 @@ def _run(grads, clip, max_norm, eps, out, workspace, norm):
         norm = torch.empty(1, dtype=torch.float32, device=dev)
     elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
         _fail("norm must be one FP32 element on %s", dev)
-    _call(dev, N.LIB.mgs_grad_norm, len(grads), table, norm.data_ptr(), workspace.data_ptr(),
+    _call(dev, N.LIB.mgs_grad_norm, len(grads), at, norm.data_ptr(), workspace.data_ptr(),
           workspace.numel() * workspace.element_size(), int(clip), float(max_norm), float(eps))
     return norm
 
@@ -69,8 +78,8 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
 
 
 def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
-    """Scales `grads` by min(1, max_norm / (norm + eps)), in place or into `out` (tensors of the same shapes, BF16 or
-    FP32), and returns the norm before that.  A NaN norm makes every result NaN, an infinite one zeros (NaN where the
+    """Scales `grads` by min(1, max_norm / (norm + eps)), in place or into `out` (contiguous tensors of as many elements,
+    BF16 or FP32), and returns the norm before that.  A NaN norm makes every result NaN, an infinite one zeros (NaN where the
     gradient is infinite)."""
     grads = list(grads)
     if stream is not None:

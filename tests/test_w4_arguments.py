@@ -89,22 +89,22 @@ def grads(*rows):
     ([(FAKE, FAKE, -1, 0, 0)], {}, "numel is negative"), ([(None, FAKE, 4, 0, 0)], {}, "grad is NULL"), ([(FAKE, FAKE, 4, 5, 0)], {}, "unknown dtype"),
     ([(FAKE + 1, FAKE, 4, 0, 0)], {}, "not aligned"), ([(FAKE, FAKE + 2, 4, 0, 1)], {}, "not aligned"),
     ([(FAKE, None, 4, 0, 0)], {}, "out is NULL"), ([(FAKE, FAKE, 4, 0, 0)], dict(norm=None), "norm is NULL"),
-    ([(FAKE, FAKE, 4, 0, 0)], dict(wb=7), "workspace of 8"), ([(FAKE, FAKE, 4, 0, 0)], dict(ws=None), "workspace of 8"),
+    ([(FAKE, FAKE, 4, 0, 0)], dict(wb=15), "workspace of 16"), ([(FAKE, FAKE, 4, 0, 0)], dict(ws=None), "workspace of 16"),
     ([(FAKE, FAKE, 4, 0, 0)], dict(max_norm=-1.0), "max_norm"), ([(FAKE, FAKE, 4, 0, 0)], dict(max_norm=float("inf")), "max_norm"),
-    ([(FAKE, FAKE, 4, 0, 0)], dict(eps=float("nan")), "eps"), ([(FAKE, FAKE, 4, 0, 0)] * 2, dict(wb=16), "overlap"),
-    ([(FAKE, FAKE, 4, 1, 0)], {}, "overlap"), ([(FAKE, FAKE + 8, 4, 0, 0), (FAKE + 14, FAKE + 14, 4, 0, 0)], dict(wb=16), "overlap"),
+    ([(FAKE, FAKE, 4, 0, 0)], dict(eps=float("nan")), "eps"), ([(FAKE, FAKE, 4, 0, 0)] * 2, dict(wb=24), "overlap"),
+    ([(FAKE, FAKE, 4, 1, 0)], {}, "overlap"), ([(FAKE, FAKE + 8, 4, 0, 0), (FAKE + 14, FAKE + 14, 4, 0, 0)], dict(wb=24), "overlap"),
     ([(FAKE, FAKE, 4, 0, 0)], dict(norm=FAKE + 4), "overlap"), ([(FAKE, FAKE, 4, 0, 0)], dict(norm=FAKE << 4), "overlap"),
 ])
 def test_norm(rows, kw, match):
-    a = dict(norm=FAKE << 8, ws=FAKE << 4, wb=8, max_norm=1.0, eps=0.0)
+    a = dict(norm=FAKE << 8, ws=FAKE << 4, wb=16, max_norm=1.0, eps=0.0)
     a.update(kw)
     rc, msg = _call("mgs_grad_norm", len(rows), grads(*rows), a["norm"], a["ws"], a["wb"], 1, a["max_norm"], a["eps"], 0)
     assert rc < 0 and match in msg, (rc, msg)
 
 
 def test_norm_workspace():
-    assert _call("mgs_grad_norm_workspace_bytes", 3, grads((FAKE, None, 65537, 0, 0), (None, None, 0, 1, 1), (FAKE, None, 1, 1, 1)))[0] == 24
-    assert _call("mgs_grad_norm_workspace_bytes", 0, None)[0] == 0
+    assert _call("mgs_grad_norm_workspace_bytes", 3, grads((FAKE, None, 2049, 0, 0), (None, None, 0, 1, 1), (FAKE, None, 1, 1, 1)))[0] == 32
+    assert _call("mgs_grad_norm_workspace_bytes", 0, None)[0] == 8
     rc, msg = _call("mgs_grad_norm_workspace_bytes", -1, None)
     assert rc < 0 and "negative" in msg
 
