@@ -21,6 +21,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "lds_dma.h"
 #include "mgs_device.h"
 #include "mgs_span.h"
 
@@ -33,8 +34,6 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef int sdesc_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) uint8_t lds8;
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) v4i lds_v4i;
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -43,7 +42,6 @@ typedef __attribute__((address_space(3))) v4f lds_f4;
 enum { EPI_PLAIN = 0, EPI_GATED_FWD = 1, EPI_GATED_BWD = 2 };
 constexpr int KSTEP = 64;           // elements of a K step: 128 bytes of a k-contiguous row
 constexpr int TILE_BLOCK_N = 4;     // tile columns of a block of the tile order
-constexpr uint32_t OUT = 0x80000000u;  // past every record count: reads zeros, without a memory access
 
 struct BfArgs {
   int mode;               // mgs_gemm_mode
@@ -153,26 +151,6 @@ __device__ __forceinline__ Job make_job(const BfArgs& ga, const Table& tt, int t
 
 // ------------------------------------------------------------------------------------ loads and MFMAs
 
-// Raw buffer descriptor of `bytes` bytes at `p` (record count capped at 2^31 - 1) in scalar registers.
-__device__ __forceinline__ sdesc_t view(const uint8_t* p, int64_t bytes) {
-  bytes = bytes < 0 ? 0 : (bytes > 0x7FFFFFFFll ? 0x7FFFFFFFll : bytes);
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  const int n = __builtin_amdgcn_readfirstlane((int)bytes);
-  return sdesc_t{(int)lo, (int)(hi & 0xffffu), n, 0x00020000};
-}
-
-// Direct-to-LDS load of 16 bytes per lane to LDS byte address `lds` + 16 x lane, in inline assembly: the
-// compiler would otherwise make later reads of the other stages wait for it.  It does not count it either;
-// every wait is an explicit one.  The whole offset is in the lanes', so that the record count bounds it.
-__device__ __forceinline__ void dma16(const sdesc_t& d, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :: "v"(voff), "s"(d), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-
 // The 4 x 4 fragments of a large tile fill the AGPRs: written as inline assembly, with the accumulators pinned
 // there, since the register allocator otherwise keeps part of them elsewhere and spills.  The compiler does not
 // see these as MFMAs, so mfma_gap() stands between VALU writes of accumulators and the first one, and
@@ -272,14 +250,13 @@ struct Operand {
       }
     }
   }
-  // before the loads of step st.  A descriptor that a VALU instruction has just written to scalar registers needs
-  // five wait states before a load reads it, and the compiler does not see the loads: it is final here.
+  // before the loads of step st
   __device__ __forceinline__ void begin(int st) {
     if constexpr (!KC) {
       const int64_t rem = k - (int64_t)st * KSTEP;
       desc = view(base + (int64_t)st * KSTEP * ld, rem > 0 ? rem * ld - col : 0);
     }
-    asm volatile("s_nop 4" ::"s"(desc));
+    desc_final(desc);
   }
   // load n (0 .. LOADS - 1) of step st to the operand's part of a stage
   __device__ __forceinline__ void load(int st, uint32_t lds, int wave, int n) const {
@@ -603,7 +580,9 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
   const uint32_t ch[2] = {(uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4), (uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4) ^ 64u};
   for (int64_t m0 = r0; m0 < r1; m0 += TM) {
     const sdesc_t ad = view(reinterpret_cast<const uint8_t*>(ga.a) + m0 * ld, (r1 - m0) * ld);
-    asm volatile("s_nop 4" ::"s"(ad), "s"(bd0), "s"(bd1));  // (see Operand::begin)
+    desc_final(ad);
+    desc_final(bd0);
+    desc_final(bd1);
     auto issue = [&](int i) {  // the wave's i-th unit into slot i % D
       const int64_t k0 = 128 * (int64_t)(wave + WAVES * i);
       const uint32_t dst = ring_at + (uint32_t)(i % D) * UNIT;

@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "lds_dma.h"
 #include "mgs_device.h"
 #include "mgs_span.h"
 
@@ -27,7 +28,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int W4_ROWS = 16, W4_K = 128;
-constexpr uint32_t OUT = 0x80000000u;  // past every record count: reads zeros
 
 // Bytes of a block: codes, then [16 rows][groups] of scales (BF16), or of dwords with the scale in the upper half and
 // the BF16 number 16 + z in the lower one.
@@ -48,21 +48,18 @@ struct W4Args {
   int c_f32;
 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)min<int64_t>(bytes, 0x7fffffff), 0x00020000);
-}
-
 template <int G, bool Z>
-struct Meta {  // the lane's scales of a block, as they are loaded
+struct Meta {  // the lane's scales of a block
   v4u d;
-  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    if constexpr (G * (Z ? 4 : 2) == 2) d[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
-    else if constexpr (G * (Z ? 4 : 2) == 4) d[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
-    else if constexpr (G * (Z ? 4 : 2) == 8) {
-      const v2u v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+  __device__ __forceinline__ void read(const lds8* p) {
+    constexpr int B = G * (Z ? 4 : 2);
+    if constexpr (B == 2) d[0] = *reinterpret_cast<const __attribute__((address_space(3))) uint16_t*>(p);
+    else if constexpr (B == 4) d[0] = *reinterpret_cast<const __attribute__((address_space(3))) uint32_t*>(p);
+    else if constexpr (B == 8) {
+      const v2u v = *reinterpret_cast<const __attribute__((address_space(3))) v2u*>(p);
       d[0] = v[0]; d[1] = v[1];
     } else {
-      d = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+      d = *reinterpret_cast<const __attribute__((address_space(3))) v4u*>(p);
     }
   }
   __device__ __forceinline__ float scale(int g) const {
@@ -86,51 +83,59 @@ __device__ __forceinline__ v8bf weights8(uint32_t w) {
   return __builtin_bit_cast(v8bf, r);
 }
 
-// A workgroup owns 16 NT weight rows (the gated form: 16 gate rows and the same up rows, NT = 2) of one expert and all
-// of its x rows, 16 MT at a time; its waves take the blocks along k in turn, D of them under way, and the partial
-// results are added in wave order through LDS.  G: groups of a block.
-template <bool GATED, int MT, int NT, int G, bool Z, int WAVES, int D>
-__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a, GroupTable gt) {
-  constexpr int BLOCK = w4_block_bytes(W4_K / G, Z), MB = G * (Z ? 4 : 2), TN = GATED ? 16 : 16 * NT;
-  __shared__ __attribute__((aligned(16))) float part[WAVES][16 * NT][16 * MT + 4];
+// A workgroup owns 16 NT weight rows (the gated form: 8 NT gate rows and the same up rows) of one expert and all
+// XR of its x rows at a time (further rows are another workgroup's, up to `passes` of them); its waves take the blocks along k in turn, each through an LDS ring of D blocks of its
+// own that direct-to-LDS loads fill (weights, scales, and the 128 elements of each x row that go with them), and
+// wait for the oldest block only.  The partial results are added in wave order through LDS.  Blocks past the end are
+// loaded masked, which keeps the wait the same.  G: groups of a block.
+template <bool GATED, int XR, int NT, int G, bool Z, int WAVES, int D>
+__global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a, GroupTable gt, int passes) {
+  constexpr int MT = XR > 16 ? XR / 16 : 1;
+  constexpr int BLOCK = w4_block_bytes(W4_K / G, Z), MB = G * (Z ? 4 : 2), TN = GATED ? 8 * NT : 16 * NT;
+  constexpr int XAT = NT * 1280, UNIT = XAT + XR * 256, LOADS = 2 * NT + XR / 4;
+  constexpr int RING = WAVES * D * UNIT, PART = WAVES * 16 * NT * (16 * MT + 4) * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PART ? RING : PART];
+  auto part = reinterpret_cast<float(*)[16 * NT][16 * MT + 4]>(smem);
   const int ntn = (int)((a.n + TN - 1) / TN);
-  const int g = blockIdx.x / ntn, tn = blockIdx.x - g * ntn;
+  const int tiles = ntn * gt.num_groups, pass = blockIdx.x / tiles, tile = blockIdx.x - pass * tiles;
+  const int g = tile / ntn, tn = tile - g * ntn;
   const GroupTable& t = gt.dev ? *gt.dev : gt;
   // (wave-uniform, which the compiler cannot tell of a device table's entries: the descriptors are made of them)
   const int64_t r0 = __builtin_amdgcn_readfirstlane(t.row_off[g]), r1 = __builtin_amdgcn_readfirstlane(t.row_off[g + 1]);
-  if (r0 == r1) return;
+  if (r0 + (int64_t)pass * XR >= r1) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
+  lds8* ring = (lds8*)smem + wave * D * UNIT;
+  const uint32_t ring_at = (uint32_t)(uintptr_t)ring;
   // the weight blocks of the workgroup: rows of blocks tn NT .. (gated: tn and its up rows')
-  __amdgpu_buffer_rsrc_t wd[NT];
+  sdesc_t wd[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int64_t row = GATED ? (n ? a.n / 16 + tn : tn) : (int64_t)tn * NT + n;
-    const bool there = GATED || row < a.wtiles;
-    wd[n] = rsrc(a.w + (g * a.wtiles + (there ? row : 0)) * (int64_t)a.ktiles * BLOCK, there ? (int64_t)a.ktiles * BLOCK : 0);
+    const int64_t half = GATED ? a.n / 16 : a.wtiles;  // blocks of rows of one half
+    const int64_t i = GATED ? (int64_t)tn * (NT / 2) + n % (NT / 2) : (int64_t)tn * NT + n;
+    const bool there = i < half;
+    const int64_t row = GATED && n >= NT / 2 ? half + i : i;
+    wd[n] = view(a.w + (g * a.wtiles + (there ? row : 0)) * (int64_t)a.ktiles * BLOCK, there ? (int64_t)a.ktiles * BLOCK : 0);
+    desc_final(wd[n]);
   }
   const int64_t ld = 2 * a.k;
-  for (int64_t m0 = r0; m0 < r1; m0 += 16 * MT) {
-    const int rows = (int)min<int64_t>(16 * MT, r1 - m0);
-    const __amdgpu_buffer_rsrc_t xd = rsrc(reinterpret_cast<const uint8_t*>(a.x) + m0 * ld, rows * ld);
-    v4u wb[D][NT], xb[D][MT][4];
-    Meta<G, Z> meta[D][NT];
-    auto load = [&](int u, int kt) {  // block kt into buffer u; past the end zeros, without memory traffic
-      const bool in = kt < a.ktiles;
+  const uint32_t xc = (uint32_t)(((lane & 15) ^ (q << 2)) << 4);  // the chunk that belongs at the lane's position of row 4 i + q
+  const bool has_meta = 4 * lane < 16 * MB;
+  for (int64_t m0 = r0 + (int64_t)pass * XR; m0 < r1; m0 += (int64_t)passes * XR) {
+    const int rows = (int)min<int64_t>(XR, r1 - m0);
+    const sdesc_t xd = view(reinterpret_cast<const uint8_t*>(a.x) + m0 * ld, rows * ld);
+    desc_final(xd);
+    auto issue = [&](int i) {  // the wave's i-th block into slot i % D
+      const int kt = wave + WAVES * i;
+      const uint32_t dst = ring_at + (uint32_t)(i % D) * UNIT, at = (uint32_t)kt * BLOCK, xk = (uint32_t)kt * 256 + xc;
+      const bool in = kt < a.ktiles, xin = in && xk < ld;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint32_t at = (uint32_t)kt * BLOCK;
-        wb[u][n] = __builtin_amdgcn_raw_buffer_load_b128(wd[n], (int)(in ? at + 16u * lane : OUT), 0, 2);
-        meta[u][n].load(wd[n], in ? at + 1024u + (uint32_t)(MB * r16) : OUT);
+        dma16(wd[n], in ? at + 16u * lane : OUT, dst + n * 1280);
+        dma4(wd[n], in && has_meta ? at + 1024u + 4u * lane : OUT, dst + n * 1280 + 1024);
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t k0 = (int64_t)kt * W4_K + 32 * j;  // (k is a multiple of 32)
-          xb[u][m][j] = __builtin_amdgcn_raw_buffer_load_b128(
-              xd, (int)(k0 < a.k ? (uint32_t)((16 * m + r16) * ld) + (uint32_t)(2 * k0) + 16u * q : OUT), 0, 0);
-        }
+      for (int n = 0; n < XR / 4; ++n) dma16(xd, xin ? (uint32_t)((4 * n + q) * ld) + xk : OUT, dst + XAT + n * 1024);
     };
     v4f acc[MT][NT];
 #pragma unroll
@@ -138,46 +143,66 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a, GroupTable gt)
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const v8bf ones = __builtin_bit_cast(v8bf, v4u{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+    const int nb = __builtin_amdgcn_readfirstlane((a.ktiles - wave + WAVES - 1) / WAVES);  // the wave's blocks
 #pragma unroll
-    for (int u = 0; u < D; ++u) load(u, wave + WAVES * u);
-    for (int kt = wave; kt < a.ktiles; kt += WAVES * D) {
+    for (int i = 0; i < D; ++i) issue(i);
+    for (int i = 0; i < nb; ++i) {
+      wait_loads<(D - 1) * LOADS>();
+      const lds8* u = ring + (i % D) * UNIT;
+      v4u wb[NT];
+      Meta<G, Z> meta[NT];
 #pragma unroll
-      for (int u = 0; u < D; ++u) {
+      for (int n = 0; n < NT; ++n) {
+        wb[n] = *reinterpret_cast<const __attribute__((address_space(3))) v4u*>(u + n * 1280 + 16 * lane);
+        meta[n].read(u + n * 1280 + 1024 + MB * r16);
+      }
+      v4u xb[MT][4];
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          v4f p[MT][NT], xs[MT];
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = (16 * m + r16) & (XR - 1);  // (rows that are not there are multiplied too, and not stored)
+          xb[m][j] = *reinterpret_cast<const __attribute__((address_space(3))) v4u*>(
+              u + XAT + row * 256 + (((4 * j + q) ^ ((row & 3) << 2)) << 4));
+        }
+      // the slot is read: refill it
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      issue(i + D);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        v4f p[MT][NT], xs[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          xs[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) p[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int j = 4 / G * h; j < 4 / G * (h + 1); ++j) {
+          v8bf wv[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) wv[n] = weights8(wb[n][j]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            xs[m] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            const v8bf xv = __builtin_bit_cast(v8bf, xb[m][j]);
+            xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, xs[m], 0, 0, 0);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) p[m][n] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-          }
-#pragma unroll
-          for (int j = 4 / G * h; j < 4 / G * (h + 1); ++j) {
-            v8bf wv[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) wv[n] = weights8(wb[u][n][j]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const v8bf xv = __builtin_bit_cast(v8bf, xb[u][m][j]);
-              xs[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, ones, xs[m], 0, 0, 0);
-#pragma unroll
-              for (int n = 0; n < NT; ++n) p[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv[n], p[m][n], 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const float s = meta[u][n].scale(h), z = meta[u][n].zero(h);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[m][n][i] = __builtin_fmaf(s, __builtin_fmaf(-z, xs[m][i], p[m][n][i]), acc[m][n][i]);
+            for (int n = 0; n < NT; ++n) p[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv[n], p[m][n], 0, 0, 0);
           }
         }
-        load(u, kt + WAVES * (D + u));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float s = meta[n].scale(h), z = meta[n].zero(h);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[m][n][e] = __builtin_fmaf(s, __builtin_fmaf(-z, xs[m][e], p[m][n][e]), acc[m][n][e]);
+        }
       }
     }
+    wait_loads<0>();
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -195,7 +220,7 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a, GroupTable gt)
       };
       float v = total(col);
       if constexpr (GATED) {
-        float u = total(16 + col);
+        float u = total(TN + col);
         if (a.bias) {
           v += bf16lo(a.bias[g * 2 * a.n + gc]);
           u += bf16lo(a.bias[g * 2 * a.n + a.n + gc]);
@@ -290,7 +315,7 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(int64_t groups, int gr
 
 // ------------------------------------------------------------------------------------------ launches
 
-typedef void (*W4Kernel)(W4Args, GroupTable);
+typedef void (*W4Kernel)(W4Args, GroupTable, int);
 
 template <bool GATED, int MT, int NT, int WAVES, int D>
 W4Kernel w4_of(int group, bool zeros) {
@@ -301,20 +326,82 @@ W4Kernel w4_of(int group, bool zeros) {
          : group == 64 ? w4_kernel<GATED, MT, NT, 2, false, WAVES, D> : w4_kernel<GATED, MT, NT, 4, false, WAVES, D>;
 }
 
+// x rows of a pass: the number that needs the least, counting the passes of all groups at what one costs (n = k = 4096,
+// 8 or 16 experts, groups of 128, relative to 4 rows: 53 us for a gated pass over 16 experts, 29 us for a plain one).
+// Device-resident split sizes: the host knows the capacity only, and takes the groups to be equal.
+int pass_rows(const GroupTable& gt) {
+  const int xr[4] = {4, 16, 32, 64};
+  const double cost[4] = {1.0, 1.05, 1.55, 2.6};
+  int best = 4;
+  double least = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    double c = 0.0;
+    for (int g = 0; g < gt.num_groups; ++g) {
+      const int64_t m = gt.dev ? (gt.total_rows + gt.num_groups - 1) / gt.num_groups : gt.row_off[g + 1] - gt.row_off[g];
+      c += cost[i] * (double)((m + xr[i] - 1) / xr[i]);
+    }
+    if (i == 0 || c < least) {
+      least = c;
+      best = xr[i];
+    }
+  }
+  return best;
+}
+
+// Tile and ring by the pass's rows and by how many blocks of 16 weight rows (the gated form: pairs of them) there are.
+// Where these fill the chip, fewer waves a workgroup and more weight rows that share the x rows; where they do not, more
+// waves, which split k further.  (us; 16 experts, n = k = 4096, then one expert.)  4 rows: 29.9 with 32 weight rows
+// and two waves, 33.9 with 16 and four, 43 with 16 and eight; one expert 6.0 with four waves, 5.0 with eight; gated
+// 53 with four waves, 67 with eight.  16 rows: 30.0 with 64 weight rows and two waves, 48 with 16 and four; one
+// expert 6.2 with eight waves, 15.6 with 64 weight rows; four experts x 7160 x 2080 in groups of 32 15.3 with 32 weight
+// rows and four waves, 17.7 with eight, 18.4 with 16 weight rows; gated 55 with 64, 64 with 32; one expert 7.7 with eight
+// waves, 11.8 with two.  32 rows: 22.7 (8 experts) with 64, 31.7 with 32; one expert 6.9 with 16 weight rows and eight
+// waves, 11.6 with 64; gated 42 and 52; one expert 8.8 and 13.1.
 int w4_launch(const W4Args& a, bool gated, int group, bool zeros, const GroupTable& gt, hipStream_t st) {
-  int64_t most = 0;
-  if (gt.dev) most = std::min<int64_t>(gt.total_rows, std::max<int64_t>(16, 2 * (int64_t)gt.total_rows / gt.num_groups));
-  else
-    for (int g = 0; g < gt.num_groups; ++g) most = std::max<int64_t>(most, gt.row_off[g + 1] - gt.row_off[g]);
-  const int nt = most <= 16 ? 1 : 2;
-  const int64_t tn = gated ? 16 : 16 * nt;
-  const int64_t grid = (a.n + tn - 1) / tn * gt.num_groups;
-  if (grid > INT32_MAX / 256) return fail(MGS_ERR_SHAPE, "too many tiles");
+  const int xr = pass_rows(gt);
+  const int64_t tiles = (a.n + 15) / 16 * gt.num_groups;
+  const bool many = tiles >= (gated ? 1024 : 2048), some = tiles >= 512;
   W4Kernel kern;
-  int waves = 4;
-  if (gated) kern = most <= 16 ? w4_of<true, 1, 2, 4, 2>(group, zeros) : w4_of<true, 2, 2, 4, 1>(group, zeros);
-  else kern = most <= 16 ? w4_of<false, 1, 1, 4, 4>(group, zeros) : w4_of<false, 2, 2, 4, 1>(group, zeros);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * waves), 0, st, a, gt);
+  int waves = 4, nt = 2;
+  if (gated) {
+    if (xr == 4) {
+      if (many) kern = w4_of<true, 4, 2, 4, 2>(group, zeros);
+      else kern = w4_of<true, 4, 2, 8, 2>(group, zeros), waves = 8;
+    } else if (xr == 16) {
+      if (many) kern = w4_of<true, 16, 4, 4, 1>(group, zeros), nt = 4;
+      else kern = w4_of<true, 16, 2, 8, 1>(group, zeros), waves = 8;
+    } else if (xr == 32) {
+      if (many) kern = w4_of<true, 32, 4, 4, 1>(group, zeros), nt = 4;
+      else kern = w4_of<true, 32, 2, 8, 1>(group, zeros), waves = 8;
+    } else {
+      kern = w4_of<true, 64, 2, 4, 1>(group, zeros);
+    }
+  } else if (xr == 4) {
+    if (many) kern = w4_of<false, 4, 2, 2, 2>(group, zeros), waves = 2;
+    else if (some) kern = w4_of<false, 4, 1, 4, 2>(group, zeros), nt = 1;
+    else kern = w4_of<false, 4, 1, 8, 2>(group, zeros), nt = 1, waves = 8;
+  } else if (xr == 16) {
+    if (many) kern = w4_of<false, 16, 4, 2, 2>(group, zeros), nt = 4, waves = 2;
+    else if (some) kern = w4_of<false, 16, 2, 4, 1>(group, zeros);
+    else kern = w4_of<false, 16, 1, 8, 1>(group, zeros), nt = 1, waves = 8;
+  } else if (xr == 32) {
+    if (many) kern = w4_of<false, 32, 4, 4, 1>(group, zeros), nt = 4;
+    else if (some) kern = w4_of<false, 32, 2, 4, 1>(group, zeros);
+    else kern = w4_of<false, 32, 1, 8, 1>(group, zeros), nt = 1, waves = 8;
+  } else {
+    kern = w4_of<false, 64, 2, 4, 1>(group, zeros);
+  }
+  const int64_t tn = gated ? 8 * nt : 16 * nt;
+  // workgroups that share the passes of a group (61 rows over four experts: 15.3 us, 17.6 in one workgroup each; 512
+  // rows of one expert: 36.6 and 47.9 us)
+  int64_t passes = 1;
+  if (gt.dev) passes = gt.total_rows > xr ? 2 : 1;
+  else
+    for (int g = 0; g < gt.num_groups; ++g) passes = std::max<int64_t>(passes, (gt.row_off[g + 1] - gt.row_off[g] + xr - 1) / xr);
+  passes = std::min<int64_t>(passes, 16);
+  const int64_t grid = (a.n + tn - 1) / tn * gt.num_groups * passes;
+  if (grid > INT32_MAX / 1024) return fail(MGS_ERR_SHAPE, "too many tiles");
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * waves), 0, st, a, gt, (int)passes);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(MGS_ERR_HIP, "HIP launch error: %s", hipGetErrorString(e));
   return ok();
