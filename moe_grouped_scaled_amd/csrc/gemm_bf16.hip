@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "lds_dma.h"
 #include "mgs_device.h"
@@ -175,16 +176,6 @@ template <bool NT>
 __device__ __forceinline__ void st_bf16x8(uint16_t* p, const float (&v)[8]) {
   st16<NT>(p, v4u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])});
 }
-__device__ __forceinline__ void ld_bf16x8(const uint16_t* p, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(p), v);
-}
-
-__device__ __forceinline__ void ld_lds8(const lds8* p, float (&v)[8]) {
-  const v4f x = *reinterpret_cast<const lds_f4*>(p), y = *reinterpret_cast<const lds_f4*>(p + 16);
-  v[0] = x[0]; v[1] = x[1]; v[2] = x[2]; v[3] = x[3];
-  v[4] = y[0]; v[5] = y[1]; v[6] = y[2]; v[7] = y[3];
-}
-
 __device__ __forceinline__ float act_gated_of(int kind, float g, float u, const ActArgs& aa) {
   return kind == MGS_ACT_SWIGLU ? act_gated<MGS_ACT_SWIGLU>(g, u, aa)
          : kind == MGS_ACT_GLU  ? act_gated<MGS_ACT_GLU>(g, u, aa)
@@ -287,120 +278,204 @@ struct Operand {
 
 // ------------------------------------------------------------------------------------------ epilogues
 //
-// A wave's 32 rows at a time go through its part of LDS as FP32 and leave it by rows: eight columns a lane, 16
-// bytes of a BF16 row.
-template <int MODE, int EPI, int F>
-__device__ __forceinline__ void epilogue(const Job& j, const BfArgs& ga, v16f (&acc)[F][F], lds8* buf, int wm, int wn,
-                                         int lane) {
-  constexpr bool NT = F == 4;
-  constexpr int W = 32 * F, PITCH = W * 4 + 16;
-  constexpr int OC = EPI == EPI_GATED_FWD ? W / 2 : W;  // output columns of the wave
-  constexpr int LPR = OC / 8, RPP = 64 / LPR;           // lanes per row, rows per pass
-  const int r32 = lane & 31, h32 = lane >> 5, lr = lane / LPR, lc = 8 * (lane % LPR);
-  const int col = wn * OC + lc;                         // in the tile
-  const bool cok = col < j.cols;                        // (widths are multiples of 8)
-  const int64_t gc = j.ccol0 + col;
-  float bias[8] = {}, bias2[8] = {};
-  if (ga.bias && cok) {
-    if constexpr (EPI == EPI_GATED_FWD) {
-      ld_bf16x8(ga.bias + (int64_t)j.g * 2 * ga.n + gc, bias);
-      ld_bf16x8(ga.bias + (int64_t)j.g * 2 * ga.n + ga.n + gc, bias2);
-    } else if constexpr (EPI == EPI_PLAIN) {
-      ld_bf16x8(ga.bias + (int64_t)j.g * ga.n + gc, bias);
-    }
+// A wave's 32 rows at a time go through its part of LDS and leave it by rows, 16 bytes a lane: stored from the
+// accumulators, an instruction would write 32 bytes of each of 32 rows.  Lane (r32, h32) holds, for fragment
+// (fm, fn) and register group g, row 32 fm + r32 and the four columns 32 fn + 8 g + 4 h32 .. + 3.
+// f(0) .. f(N - 1) with the index a constant: accumulators indexed by a loop that the compiler leaves rolled would go to
+// scratch.
+template <int N, int I = 0, typename Fn>
+__device__ __forceinline__ void unrolled(Fn&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
   }
+}
+
+// Row fragment fm of the accumulators as 32 FP32 rows.  The 16-byte chunk c of row r stands at position c ^ (r & 15)
+// (of the 8 chunks of a 32-column row, F = 1: r & 7), which spreads both the writes, one chunk of every row, and the
+// reads, every second chunk of a row, evenly over the banks.
+template <int F>
+constexpr int STAGED_ROW = 128 * F;
+template <int F>
+__device__ __forceinline__ lds8* staged(lds8* buf, int row, int chunk) {
+  return buf + row * STAGED_ROW<F> + ((chunk ^ (row & (F == 1 ? 7 : 15))) << 4);
+}
+template <int F>
+__device__ __forceinline__ void stage_f32(const v16f (&acc)[F], lds8* buf, int lane) {
+  const int r32 = lane & 31, h32 = lane >> 5;
+  asm volatile("" ::: "memory");  // a wave's LDS accesses execute in order; this keeps the compiler's order
 #pragma unroll
-  for (int fm = 0; fm < F; ++fm) {
-    const int row0 = (wm * F + fm) * 32;
-    if (row0 >= j.rows) continue;
+  for (int fn = 0; fn < F; ++fn)
 #pragma unroll
-    for (int fn = 0; fn < F; ++fn)
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<lds_f4*>(staged<F>(buf, r32, 8 * fn + 2 * g + h32)) =
+          v4f{acc[fn][4 * g], acc[fn][4 * g + 1], acc[fn][4 * g + 2], acc[fn][4 * g + 3]};
+  asm volatile("" ::: "memory");
+}
+// eight columns from col on (a multiple of 8) of a staged row
+template <int F>
+__device__ __forceinline__ void staged8(lds8* buf, int row, int col, float (&v)[8]) {
+  const v4f x = *reinterpret_cast<const lds_f4*>(staged<F>(buf, row, col / 4)), y = *reinterpret_cast<const lds_f4*>(staged<F>(buf, row, col / 4 + 1));
+  v[0] = x[0]; v[1] = x[1]; v[2] = x[2]; v[3] = x[3];
+  v[4] = y[0]; v[5] = y[1]; v[6] = y[2]; v[7] = y[3];
+}
+__device__ __forceinline__ void add_bf16x8(float (&v)[8], const uint4& w) {
+  v[0] += bf16lo(w.x); v[1] += bf16hi(w.x); v[2] += bf16lo(w.y); v[3] += bf16hi(w.y);
+  v[4] += bf16lo(w.z); v[5] += bf16hi(w.z); v[6] += bf16lo(w.w); v[7] += bf16hi(w.w);
+}
+
+// The gated forward: a wave's staged rows are 16 F gate columns and the same up columns.
+template <int KIND, int F>
+__device__ __forceinline__ void gated_fwd_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
+  constexpr bool NT = F == 4;
+  constexpr int W = 16 * F, LPR = W / 8, RPP = 64 / LPR;
+  const int lr = lane / LPR, lc = lane % LPR, col = wn * W + 8 * lc;
+  if (col >= j.cols) return;
+  const int64_t gc = j.ccol0 + col;
+  uint4 bg = make_uint4(0, 0, 0, 0), bu = bg;
+  if (ga.bias) {
+    const uint16_t* b = ga.bias + (int64_t)j.g * 2 * ga.n + gc;
+    bg = *reinterpret_cast<const uint4*>(b);
+    bu = *reinterpret_cast<const uint4*>(b + ga.n);
+  }
+#pragma unroll RPP < 32 ? 2 : 1
+  for (int i = 0; i < 32 / RPP; ++i) {
+    const int row = RPP * i + lr;
+    if (row0 + row >= j.rows) continue;
+    const int64_t gr = j.crow0 + row0 + row;
+    float v[8], u[8], h[8];
+    staged8<F>(buf, row, 8 * lc, v);
+    staged8<F>(buf, row, W + 8 * lc, u);
+    const float s = ga.probs ? ga.probs[gr] : 1.0f;
+    add_bf16x8(v, bg);
+    add_bf16x8(u, bu);
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<lds_f4*>(buf + r32 * PITCH + 4 * (fn * 32 + 8 * g + 4 * h32)) =
-            v4f{acc[fm][fn][4 * g], acc[fm][fn][4 * g + 1], acc[fm][fn][4 * g + 2], acc[fm][fn][4 * g + 3]};
-    // a wave's LDS accesses execute in order; this keeps the compiler's order
-    asm volatile("" ::: "memory");
-#pragma unroll 2
-    for (int i = 0; i < 32 / RPP; ++i) {
-      const int row = RPP * i + lr;
-      const lds8* p = buf + row * PITCH + 4 * lc;
-      float v[8];
-      ld_lds8(p, v);
-      const bool ok = cok && row0 + row < j.rows;
-      const int64_t gr = j.crow0 + row0 + row;
-      if constexpr (EPI == EPI_PLAIN) {
-        if (!ok) continue;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] += bias[t];
-        if (ga.c_f32) {
-          float* c = reinterpret_cast<float*>(ga.c) + gr * ga.n + gc;
-          if (ga.accumulate) {
-            const float4 x = *reinterpret_cast<const float4*>(c), y = *reinterpret_cast<const float4*>(c + 4);
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-          }
-          st16<NT>(c, v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-          st16<NT>(c + 4, v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
-        } else {
-          st_bf16x8<NT>(reinterpret_cast<uint16_t*>(ga.c) + gr * ga.n + gc, v);
-        }
-      } else if constexpr (EPI == EPI_GATED_FWD) {
-        if (!ok) continue;
-        float u[8], h[8];
-        ld_lds8(p + 4 * OC, u);
-        const float s = ga.probs ? ga.probs[gr] : 1.0f;
+    for (int t = 0; t < 8; ++t) h[t] = act_gated<KIND>(v[t], u[t], ga.act) * s;
+    st_bf16x8<NT>(static_cast<uint16_t*>(ga.c) + gr * ga.n + gc, h);
+    if (ga.pre_out) {
+      if constexpr (KIND == MGS_ACT_CLAMPED_SWIGLU) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-          v[t] += bias[t];
-          u[t] += bias2[t];
-          h[t] = act_gated_of(ga.act.kind, v[t], u[t], ga.act) * s;
-        }
-        st_bf16x8<NT>(reinterpret_cast<uint16_t*>(ga.c) + gr * ga.n + gc, h);
-        if (ga.pre_out) {
-          if (ga.act.kind == MGS_ACT_CLAMPED_SWIGLU) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              v[t] = same_side_gate(v[t], ga);
-              u[t] = same_side(u[t], ga);
-            }
-          }
-          st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + gc, v);
-          st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + ga.n + gc, u);
-        }
-      } else {
-        float dp = 0.0f;
-        if (ok) {
-          float g[8], u[8], dg[8], du[8], h[8];
-          ld_bf16x8(ga.pre + gr * 2 * ga.n + gc, g);
-          ld_bf16x8(ga.pre + gr * 2 * ga.n + ga.n + gc, u);
-          const float s = ga.probs ? ga.probs[gr] : 1.0f;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            float a, bg, bu;
-            if (ga.act.kind == MGS_ACT_SWIGLU) dact_gated<MGS_ACT_SWIGLU>(g[t], u[t], ga.act, a, bg, bu);
-            else if (ga.act.kind == MGS_ACT_GLU) dact_gated<MGS_ACT_GLU>(g[t], u[t], ga.act, a, bg, bu);
-            else dact_gated<MGS_ACT_CLAMPED_SWIGLU>(g[t], u[t], ga.act, a, bg, bu);
-            dp += v[t] * a;
-            dg[t] = v[t] * s * bg;
-            du[t] = v[t] * s * bu;
-            h[t] = a * s;
-          }
-          uint16_t* d = reinterpret_cast<uint16_t*>(ga.c) + gr * 2 * ga.n + gc;
-          st_bf16x8<NT>(d, dg);
-          st_bf16x8<NT>(d + ga.n, du);
-          if (ga.h_out) st_bf16x8<NT>(ga.h_out + gr * ga.n + gc, h);
-        }
-        if (ga.dp_part) {
-          // over the row's LPR lanes, in a fixed order
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) dp += __shfl_xor(dp, o);
-          if (lane % LPR == 0 && row0 + row < j.rows) ga.dp_part[gr * ga.dp_ld + 2 * j.tn + wn] = dp;
+          v[t] = same_side_gate(v[t], ga);
+          u[t] = same_side(u[t], ga);
         }
       }
+      st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + gc, v);
+      st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + ga.n + gc, u);
     }
-    asm volatile("" ::: "memory");
   }
+}
+
+// The gated backward: da beside what the forward saved of the same eight columns, which is loaded one pass ahead.
+template <int KIND, int F>
+__device__ __forceinline__ void gated_bwd_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
+  constexpr bool NT = F == 4;
+  constexpr int W = 32 * F, LPR = W / 8, RPP = 64 / LPR;
+  const int lr = lane / LPR, lc = lane % LPR;
+  const bool cok = wn * W + 8 * lc < j.cols;
+  const int64_t gc = j.ccol0 + wn * W + 8 * lc, ld = 2 * ga.n, gr0 = j.crow0 + row0;
+  struct Saved { uint4 g, u; float s; };
+  auto saved = [&](int row) {
+    Saved x{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), 1.0f};
+    if (cok && row < 32 && row0 + row < j.rows) {
+      const uint16_t* p = ga.pre + (gr0 + row) * ld + gc;
+      x.g = *reinterpret_cast<const uint4*>(p);
+      x.u = *reinterpret_cast<const uint4*>(p + ga.n);
+      if (ga.probs) x.s = ga.probs[gr0 + row];
+    }
+    return x;
+  };
+  Saved next = saved(lr);
+#pragma unroll 2
+  for (int i = 0; i < 32 / RPP; ++i) {
+    const int row = RPP * i + lr;
+    const Saved now = next;
+    next = saved(row + RPP);
+    float v[8], g[8], u[8], dg[8], du[8], h[8], dp = 0.0f;
+    staged8<F>(buf, row, 8 * lc, v);
+    unpack8(now.g, g);
+    unpack8(now.u, u);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      float a, bg, bu;
+      dact_gated<KIND>(g[t], u[t], ga.act, a, bg, bu);
+      dp += v[t] * a;
+      const float d = v[t] * now.s;
+      dg[t] = d * bg;
+      du[t] = d * bu;
+      h[t] = a * now.s;
+    }
+    const bool ok = cok && row0 + row < j.rows;
+    const int64_t gr = gr0 + row;
+    if (ok) {
+      uint16_t* d = static_cast<uint16_t*>(ga.c) + gr * ld + gc;
+      st_bf16x8<NT>(d, dg);
+      st_bf16x8<NT>(d + ga.n, du);
+      if (ga.h_out) st_bf16x8<NT>(ga.h_out + gr * ga.n + gc, h);
+    }
+    if (ga.dp_part) {
+      // over the row's LPR lanes, in a fixed order (columns past the end count nothing)
+      dp = ok ? dp : 0.0f;
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) dp += __shfl_xor(dp, o);
+      if (lc == 0 && row0 + row < j.rows) ga.dp_part[gr * ga.dp_ld + 2 * j.tn + wn] = dp;
+    }
+  }
+}
+
+// C with its bias, in BF16 or FP32, optionally added to what is there.
+template <bool F32, int F>
+__device__ __forceinline__ void plain_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
+  constexpr bool NT = F == 4;
+  constexpr int W = 32 * F, LPR = W / 8, RPP = 64 / LPR;
+  const int lr = lane / LPR, lc = lane % LPR, col = wn * W + 8 * lc;
+  if (col >= j.cols) return;
+  const int64_t gc = j.ccol0 + col;
+  uint4 b = make_uint4(0, 0, 0, 0);
+  if (ga.bias) b = *reinterpret_cast<const uint4*>(ga.bias + (int64_t)j.g * ga.n + gc);
+#pragma unroll 2
+  for (int i = 0; i < 32 / RPP; ++i) {
+    const int row = RPP * i + lr;
+    float v[8];
+    staged8<F>(buf, row, 8 * lc, v);
+    add_bf16x8(v, b);
+    if (row0 + row >= j.rows) continue;
+    const int64_t at = (j.crow0 + row0 + row) * ga.n + gc;
+    if constexpr (F32) {
+      float* c = static_cast<float*>(ga.c) + at;
+      if (ga.accumulate) {
+        const float4 x = *reinterpret_cast<const float4*>(c), y = *reinterpret_cast<const float4*>(c + 4);
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+      }
+      st16<NT>(c, v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+      st16<NT>(c + 4, v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+    } else {
+      st_bf16x8<NT>(static_cast<uint16_t*>(ga.c) + at, v);
+    }
+  }
+}
+
+template <int EPI, int F>
+__device__ __forceinline__ void epilogue(const Job& j, const BfArgs& ga, v16f (&acc)[F][F], lds8* buf, int wm, int wn, int lane) {
+  unrolled<F>([&](auto fm_) __attribute__((always_inline)) {
+    constexpr int fm = decltype(fm_)::value;
+    const int row0 = (wm * F + fm) * 32;
+    if (row0 >= j.rows) return;
+    stage_f32<F>(acc[fm], buf, lane);
+    if constexpr (EPI == EPI_GATED_FWD) {
+      if (ga.act.kind == MGS_ACT_SWIGLU) gated_fwd_rows<MGS_ACT_SWIGLU, F>(j, ga, buf, row0, wn, lane);
+      else if (ga.act.kind == MGS_ACT_GLU) gated_fwd_rows<MGS_ACT_GLU, F>(j, ga, buf, row0, wn, lane);
+      else gated_fwd_rows<MGS_ACT_CLAMPED_SWIGLU, F>(j, ga, buf, row0, wn, lane);
+    } else if constexpr (EPI == EPI_GATED_BWD) {
+      if (ga.act.kind == MGS_ACT_SWIGLU) gated_bwd_rows<MGS_ACT_SWIGLU, F>(j, ga, buf, row0, wn, lane);
+      else if (ga.act.kind == MGS_ACT_GLU) gated_bwd_rows<MGS_ACT_GLU, F>(j, ga, buf, row0, wn, lane);
+      else gated_bwd_rows<MGS_ACT_CLAMPED_SWIGLU, F>(j, ga, buf, row0, wn, lane);
+    } else {
+      if (ga.c_f32) plain_rows<true, F>(j, ga, buf, row0, wn, lane);
+      else plain_rows<false, F>(j, ga, buf, row0, wn, lane);
+    }
+  });
 }
 
 // ---------------------------------------------------------------------------------------- the kernel
@@ -540,7 +615,8 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
   __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_waitcnt(0);  // the masked loads of the steps past the end write LDS too
   __syncthreads();
-  epilogue<MODE, EPI, F>(j, ga, acc, lds + wave * (S * STAGE / 4), wm, wn, lane);
+  lds8* buf = lds + wave * (S * STAGE / 4);
+  epilogue<EPI, F>(j, ga, acc, buf, wm, wn, lane);
 }
 
 
@@ -552,11 +628,11 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
 // through an LDS ring of D units of its own (a row's unit is one 128-byte line), and waits for the oldest unit
 // only.  Waves share nothing until the end, where the four partial tiles are added in wave order through LDS, so
 // the result does not depend on timing.  Units past the end are loaded masked, which keeps the wait the same.
-template <int EPI, int MT, int NT, int D>
-__global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt) {
-  constexpr int TM = 16 * MT, TB = 16 * NT, TN = EPI == EPI_GATED_FWD ? TB / 2 : TB, WAVES = 4;
-  constexpr int UNIT = (MT + NT) * 2048, LOADS = 2 * (MT + NT), PITCH = TB + 4;
-  constexpr int RING = WAVES * D * UNIT, PART = WAVES * TM * PITCH * 4;
+template <int EPI, int XR, int NT, int WAVES, int D>
+__global__ __launch_bounds__(64 * WAVES) void rows_bf16_kernel(BfArgs ga, GroupTable gt) {
+  constexpr int MT = XR / 16, TB = 16 * NT, TN = EPI == EPI_GATED_FWD ? TB / 2 : TB;
+  constexpr int UNIT = NT * 2048 + XR * 128, LOADS = 2 * NT + XR / 8, PITCH = TB + 4;
+  constexpr int RING = WAVES * D * UNIT, PART = WAVES * 16 * MT * PITCH * 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING > PART ? RING : PART];
   const int ntn = (int)((ga.n + TN - 1) / TN);
   const int g = blockIdx.x / ntn, tn = blockIdx.x - g * ntn;
@@ -578,7 +654,7 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
   const sdesc_t bd1 = EPI == EPI_GATED_FWD ? view(b + (g * nb + ga.n + col0) * ld, (ga.n - col0) * ld) : bd0;
   const int lrow = lane >> 3;
   const uint32_t ch[2] = {(uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4), (uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4) ^ 64u};
-  for (int64_t m0 = r0; m0 < r1; m0 += TM) {
+  for (int64_t m0 = r0; m0 < r1; m0 += XR) {
     const sdesc_t ad = view(reinterpret_cast<const uint8_t*>(ga.a) + m0 * ld, (r1 - m0) * ld);
     desc_final(ad);
     desc_final(bd0);
@@ -594,7 +670,7 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
         dma16(n < NT ? bd0 : bd1, ok[n & 1] ? off : OUT, dst + n * 1024);
       }
 #pragma unroll
-      for (int n = 0; n < 2 * MT; ++n)
+      for (int n = 0; n < XR / 8; ++n)
         dma16(ad, ok[n & 1] ? (uint32_t)((8 * n + lrow) * ld + k0) + ch[n & 1] : OUT, dst + (2 * NT + n) * 1024);
     };
     v4f acc[MT][NT];
@@ -614,7 +690,7 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
 #pragma unroll
         for (int n = 0; n < NT; ++n) bf[n] = *reinterpret_cast<const lds_v4i*>(u + n * 2048 + at);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) af[m] = *reinterpret_cast<const lds_v4i*>(u + (NT + m) * 2048 + at);
+        for (int m = 0; m < MT; ++m) af[m] = *reinterpret_cast<const lds_v4i*>(u + NT * 2048 + m * 2048 + at);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -631,15 +707,15 @@ __global__ __launch_bounds__(256) void rows_bf16_kernel(BfArgs ga, GroupTable gt
     __builtin_amdgcn_sched_barrier(0);
     mfma_drain();
     __builtin_amdgcn_sched_barrier(0);
-    float(*part)[TM][PITCH] = reinterpret_cast<float(*)[TM][PITCH]>(smem);
+    auto part = reinterpret_cast<float(*)[16 * MT][PITCH]>(smem);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         *reinterpret_cast<v4f*>(&part[wave][16 * m + r16][16 * n + 4 * q]) = acc[m][n];
     __syncthreads();
-    const int rows = (int)min<int64_t>(TM, r1 - m0);
-    for (int i = threadIdx.x; i < TM * TN / 4; i += 256) {
+    const int rows = (int)min<int64_t>(XR, r1 - m0);
+    for (int i = threadIdx.x; i < 16 * MT * TN / 4; i += 64 * WAVES) {
       const int row = i / (TN / 4), col = 4 * (i - row * (TN / 4));
       const int64_t gr = m0 + row, gc = col0 + col;
       if (row >= rows || gc >= ga.n) continue;
@@ -815,17 +891,48 @@ int tile_side(const BfArgs& ga, int epi, const GroupTable& gt) {
   return 1;
 }
 
-// f: the tile's side over 64; 0: the kernel for few rows.  Enqueues the product (the device table first, where
+// Whether workgroups of 32 weight rows (the gated form: of 16 pairs) leave CUs without two of them.
+bool few_tiles(const BfArgs& ga, int epi, const GroupTable& gt) {
+  const int64_t tn = epi == EPI_GATED_FWD ? 16 : 32;
+  return (ga.n + tn - 1) / tn * gt.num_groups < 512;
+}
+
+// x rows of a workgroup of the kernel for few rows, or 0 where the tiles are faster.  (us, gated and plain.)  One expert,
+// 4096 x 4096: 32 rows 13.8 and 10.5, 64 rows 17.0 and 11.0, on tiles 20.8 and 18.2, which 128 rows take too.  16
+// experts, 7168 x 2048: 2 rows each 153 and 82, 32 rows 162 and 90, on tiles 168 and 87; 64 rows 188 and 102, on
+// tiles 186 and 101.  With few workgroups the weight rows of one are fewer, so that more CUs read (one row, plain:
+// 9.4 against 12.2); with many and 32 rows they are more, so that the x rows are read less often (162 against 183).
+int few_rows(const BfArgs& ga, int epi, const GroupTable& gt) {
+  if (ga.mode != MGS_GEMM_FPROP) return 0;
+  const int64_t most = most_rows(gt);
+  return most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 && few_tiles(ga, epi, gt) ? 64 : 0;
+}
+
+// Enqueues the product (the device table first, where
 // the split sizes are device-resident).
 int launch(const BfArgs& ga, int epi, const GroupTable& gt, GemmTable* dev_table, hipStream_t st) {
-  if (ga.mode == MGS_GEMM_FPROP && most_rows(gt) <= 32) {
-    const bool one = most_rows(gt) <= 16;
-    const int64_t grid = (int64_t)gt.num_groups * ((ga.n + (epi == EPI_GATED_FWD ? 15 : 31)) / (epi == EPI_GATED_FWD ? 16 : 32));
-    if (grid > INT32_MAX / 256) return fail(MGS_ERR_SHAPE, "too many tiles");
-    void (*kern)(BfArgs, GroupTable) =
-        epi == EPI_GATED_FWD ? (one ? rows_bf16_kernel<EPI_GATED_FWD, 1, 2, 2> : rows_bf16_kernel<EPI_GATED_FWD, 2, 2, 2>)
-                             : (one ? rows_bf16_kernel<EPI_PLAIN, 1, 2, 2> : rows_bf16_kernel<EPI_PLAIN, 2, 2, 2>);
-    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, ga, gt);
+  if (const int xr = few_rows(ga, epi, gt)) {
+    const bool gated = epi == EPI_GATED_FWD, few = few_tiles(ga, epi, gt);
+    void (*kern)(BfArgs, GroupTable);
+    int waves = 4, tn = 32;
+    if (gated) {
+      tn = 16;
+      if (xr == 16) kern = rows_bf16_kernel<EPI_GATED_FWD, 16, 2, 4, 2>;
+      else if (xr == 64) kern = rows_bf16_kernel<EPI_GATED_FWD, 64, 2, 4, 1>;
+      else if (few) kern = rows_bf16_kernel<EPI_GATED_FWD, 32, 2, 4, 2>;
+      else kern = rows_bf16_kernel<EPI_GATED_FWD, 32, 4, 4, 1>, tn = 32;
+    } else if (few) {
+      tn = 16;
+      if (xr == 16) kern = rows_bf16_kernel<EPI_PLAIN, 16, 1, 8, 2>, waves = 8;
+      else if (xr == 32) kern = rows_bf16_kernel<EPI_PLAIN, 32, 1, 8, 2>, waves = 8;
+      else kern = rows_bf16_kernel<EPI_PLAIN, 64, 1, 4, 2>;
+    } else {
+      if (xr == 16) kern = rows_bf16_kernel<EPI_PLAIN, 16, 2, 4, 2>;
+      else kern = rows_bf16_kernel<EPI_PLAIN, 32, 4, 4, 1>, tn = 64;
+    }
+    const int64_t grid = (int64_t)gt.num_groups * ((ga.n + tn - 1) / tn);
+    if (grid > INT32_MAX / 1024) return fail(MGS_ERR_SHAPE, "too many tiles");
+    hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * waves), 0, st, ga, gt);
   } else {
     const int f = tile_side(ga, epi, gt), tm = 64 * f;
     const int64_t ntn = tile_columns(epi, ga.n, f), tiles = tile_count(ga, epi, gt, f);
