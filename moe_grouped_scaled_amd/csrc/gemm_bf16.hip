@@ -159,9 +159,26 @@ __device__ __forceinline__ Job make_job(const BfArgs& ga, const Table& tt, int t
 __device__ __forceinline__ void mfma_pinned(v16f& acc, const v4i& b, const v4i& a) {
   asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
+// the same with a load of 16 bytes a lane behind it, to LDS address `lds` + `off` (M0 is set ahead of the MFMA, which is
+// the wait state it needs before the load)
+__device__ __forceinline__ void mfma_with_load(v16f& acc, const v4i& b, const v4i& a, const sdesc_t& d, uint32_t voff, uint32_t lds,
+                                               int off) {
+  asm volatile("s_add_u32 m0, %5, %6\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0\n\tbuffer_load_dwordx4 %3, %4, 0 offen lds"
+               : "+a"(acc) : "v"(b), "v"(a), "v"(voff), "s"(d), "s"(lds), "n"(off) : "memory", "scc");
+}
 __device__ __forceinline__ void mfma_gap() { asm volatile("s_nop 7"); }
 __device__ __forceinline__ void mfma_drain() {
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7\n\ts_nop 7");
+}
+
+// f(0) .. f(N - 1) with the index a constant: accumulators indexed by a loop that the compiler leaves rolled would go to
+// scratch.
+template <int N, int I = 0, typename Fn>
+__device__ __forceinline__ void unrolled(Fn&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unrolled<N, I + 1>(f);
+  }
 }
 
 // 16-byte store whose data registers stay live through two wait states (a store wider than 8 bytes reads
@@ -196,78 +213,95 @@ __device__ __forceinline__ float same_side_gate(float v, const BfArgs& ga) {
 }
 
 // One operand of the kernel: the loads of its part of a stage, and its fragments.  T: its rows (outputs) of
-// the tile, F = T / 64 fragments a wave; KC: k-contiguous.
-template <int T, bool KC>
+// the tile, F = T / 64 fragments a wave; KC: k-contiguous; S stages.  Everything that a step's loads and reads need is
+// in registers before the loop (lane offsets, LDS addresses of every stage), so that behind an MFMA stand one or two
+// instructions: the wave is alone on its SIMD, and what does not fit behind its MFMAs holds them up.
+template <int T, bool KC, int S>
 struct Operand {
   static constexpr int F = T / 64, PITCH = 2 * T;   // bytes of a stage row (not KC)
   static constexpr int LOADS = 2 * F;               // per wave and step
   static constexpr int READS = KC ? F : 2 * F;      // LDS reads of a substep's fragments
-  const uint8_t* base;
-  int64_t ld, bytes, k, col;  // col: byte offset of the base in its row (not KC)
-  sdesc_t desc;               // KC: of the whole operand; else of one step
-  uint32_t vo[2], ch[2], inc;
-  uint32_t at[F];             // LDS offsets of the lane's fragments
+  static constexpr int ADDR = KC ? 4 : F;
+  uint64_t at;              // the next step's first byte: KC of row 0, else of its first row
+  int left;                 // KC: bytes of a row from the next step on; else rows
+  int records, ld, col;     // KC: bytes from `at` to the operand's end; not KC: bytes of a row, byte offset in it
+  sdesc_t desc;             // of one step
+  uint32_t vo[LOADS], ch;   // lane offsets of a step's loads; KC: byte of the lane's chunk in a row (even loads)
+  uint32_t dst[S];          // LDS addresses: of the wave's loads, and of the lane's fragments
+  uint32_t rd[S][ADDR];
 
-  // row0: the first of the rows that this wave loads (KC); w0: the first of those it multiplies
-  __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int64_t bytes_, int64_t k_, int64_t col_,
-                                       int row0, int w0, int wave, int lane) {
-    base = p; ld = ld_; bytes = bytes_; k = k_; col = col_;
-    const int r32 = lane & 31, h32 = lane >> 5;
+  // row0: the first of the rows that this wave loads (KC); w0: the first of those it multiplies; lds: the operand's
+  // part of stage 0, `stage` bytes apart
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int64_t bytes, int64_t k, int64_t col_, int row0, int w0,
+                                       uint32_t lds, uint32_t stage, int wave, int lane) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+    ld = __builtin_amdgcn_readfirstlane((int)ld_);
+    col = __builtin_amdgcn_readfirstlane((int)col_);
+    left = __builtin_amdgcn_readfirstlane((int)(KC ? 2 * k : k));
+    records = __builtin_amdgcn_readfirstlane((int)min<int64_t>(bytes, 0x7fffffff));
+    const int r32 = lane & 31, h32 = lane >> 5, s4 = (lane & 15) >> 2;
     if constexpr (KC) {
       const int lrow = lane >> 3;
-      ch[0] = (uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4);
-      ch[1] = ch[0] ^ 64u;
-      vo[0] = (uint32_t)((row0 + lrow) * ld) + ch[0];
-      vo[1] = (uint32_t)((row0 + lrow) * ld) + ch[1];
-      inc = (uint32_t)(8 * ld);
-      desc = view(base, bytes);
+      ch = (uint32_t)(((lane & 7) ^ (lrow >> 1)) << 4);
 #pragma unroll
-      for (int f = 0; f < F; ++f) at[f] = (uint32_t)(w0 + 32 * f + r32) * 128;
+      for (int n = 0; n < LOADS; ++n) vo[n] = (uint32_t)((row0 + 8 * n + lrow) * ld) + (ch ^ (n & 1 ? 64u : 0u));
     } else {
-      constexpr int CPR = PITCH / 16;  // chunks of a stage row
+      constexpr int CPR = PITCH / 16, RPI = 1024 / PITCH;  // chunks of a stage row, rows of a load
       const int lr = lane / CPR, pos = lane % CPR;
 #pragma unroll
-      for (int p2 = 0; p2 < 2; ++p2) {
-        const int sw = T == 64 ? (((lr >> 1) & 1) << 2) : T == 128 ? ((lr & 3) << 2) : (((2 * p2 + lr) & 3) << 2);
-        vo[p2] = (uint32_t)((16 * wave + lr) * ld) + (uint32_t)((pos ^ sw) << 4);
+      for (int n = 0; n < LOADS; ++n) {
+        const int row = 16 * wave + RPI * n + lr, sw = T == 64 ? (((row >> 1) & 1) << 2) : ((row & 3) << 2);
+        vo[n] = (uint32_t)(row * ld) + (uint32_t)((pos ^ sw) << 4);
       }
-      inc = (uint32_t)((1024 / PITCH) * ld);
-      const int s4 = (lane & 15) >> 2;
-      const int sw = T == 64 ? (((s4 >> 1) & 1) << 2) : (s4 << 2);
+    }
 #pragma unroll
-      for (int f = 0; f < F; ++f) {
-        const int chunk = (w0 + 32 * f) / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        at[f] = (uint32_t)((8 * h32 + s4) * PITCH + ((chunk ^ sw) << 4) + 8 * (lane & 1));
+    for (int n = 0; n < LOADS; ++n) asm volatile("" : "+v"(vo[n]));
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      dst[s] = __builtin_amdgcn_readfirstlane(lds + s * stage + wave * LOADS * 1024);
+#pragma unroll
+      for (int i = 0; i < ADDR; ++i) {
+        if constexpr (KC) {
+          rd[s][i] = lds + s * stage + (uint32_t)(w0 + r32) * 128 + (((2 * i + h32) ^ ((r32 >> 1) & 7)) << 4);
+        } else {
+          const int chunk = (w0 + 32 * i) / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          const int sw = T == 64 ? (((s4 >> 1) & 1) << 2) : (s4 << 2);
+          rd[s][i] = lds + s * stage + (uint32_t)((8 * h32 + s4) * PITCH + ((chunk ^ sw) << 4) + 8 * (lane & 1));
+        }
+        asm volatile("" : "+v"(rd[s][i]));
       }
     }
   }
-  // before the loads of step st
-  __device__ __forceinline__ void begin(int st) {
-    if constexpr (!KC) {
-      const int64_t rem = k - (int64_t)st * KSTEP;
-      desc = view(base + (int64_t)st * KSTEP * ld, rem > 0 ? rem * ld - col : 0);
+  // the loads from here on are the next step's (from step 0 on)
+  __device__ __forceinline__ void begin() {
+    int n;
+    if constexpr (KC) {
+      n = max(records, 0);
+      if (left < 128) {
+        // a partial step, and those behind the last: a lane whose chunk is past the row's end stays out from here on
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) vo[i] = (int)(ch ^ (i & 1 ? 64u : 0u)) < left ? vo[i] : OUT;
+      }
+    } else {
+      n = left > 0 ? min(left, KSTEP) * ld - col : 0;
     }
+    desc = sdesc_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)at), __builtin_amdgcn_readfirstlane((int)((uint32_t)(at >> 32) & 0xffffu)),
+                   __builtin_amdgcn_readfirstlane(n), 0x00020000};
+    at += KC ? 128 : (uint64_t)KSTEP * (uint32_t)ld;
+    left -= KC ? 128 : KSTEP;
+    records -= 128;
     desc_final(desc);
   }
-  // load n (0 .. LOADS - 1) of step st to the operand's part of a stage
-  __device__ __forceinline__ void load(int st, uint32_t lds, int wave, int n) const {
-    const uint32_t dst = lds + (wave * LOADS + n) * 1024;
+  // load n (0 .. LOADS - 1) of the step to stage s
+  __device__ __forceinline__ void load(int s, int n) const { dma16(desc, vo[n], dst[s] + n * 1024); }
+  // read i (0 .. READS - 1) of the fragments of substep kk of stage s
+  __device__ __forceinline__ void read(int s, int kk, int i, v4i (&fr)[F]) const {
     if constexpr (KC) {
-      const int64_t left = 2 * k - (int64_t)st * 128;  // bytes of a row from this step on
-      const uint32_t off = vo[n & 1] + (uint32_t)n * inc + (uint32_t)st * 128;
-      dma16(desc, (int64_t)ch[n & 1] < left ? off : OUT, dst);
-    } else {
-      dma16(desc, vo[n & 1] + (uint32_t)n * inc, dst);
-    }
-  }
-  // read i (0 .. READS - 1) of the fragments of substep kk
-  __device__ __forceinline__ void read(const lds8* stage, int kk, int i, v4i (&fr)[F], int lane) const {
-    if constexpr (KC) {
-      const int r32 = lane & 31, h32 = lane >> 5;
-      fr[i] = *reinterpret_cast<const lds_v4i*>(stage + at[i] + (((2 * kk + h32) ^ ((r32 >> 1) & 7)) << 4));
+      fr[i] = *reinterpret_cast<const lds_v4i*>((lds8*)(uintptr_t)rd[s][kk] + i * 32 * 128);
     } else {
       const int f = i >> 1, h = i & 1;
-      const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(stage + at[f] + (16 * kk + 4 * h) * PITCH));
+      const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)((lds8*)(uintptr_t)rd[s][f] + (16 * kk + 4 * h) * PITCH));
       typedef int v2i __attribute__((ext_vector_type(2)));
       const v2i w = __builtin_bit_cast(v2i, v);
       fr[f][2 * h] = w[0];
@@ -281,16 +315,6 @@ struct Operand {
 // A wave's 32 rows at a time go through its part of LDS and leave it by rows, 16 bytes a lane: stored from the
 // accumulators, an instruction would write 32 bytes of each of 32 rows.  Lane (r32, h32) holds, for fragment
 // (fm, fn) and register group g, row 32 fm + r32 and the four columns 32 fn + 8 g + 4 h32 .. + 3.
-// f(0) .. f(N - 1) with the index a constant: accumulators indexed by a loop that the compiler leaves rolled would go to
-// scratch.
-template <int N, int I = 0, typename Fn>
-__device__ __forceinline__ void unrolled(Fn&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    unrolled<N, I + 1>(f);
-  }
-}
-
 // Row fragment fm of the accumulators as 32 FP32 rows.  The 16-byte chunk c of row r stands at position c ^ (r & 15)
 // (of the 8 chunks of a 32-column row, F = 1: r & 7), which spreads both the writes, one chunk of every row, and the
 // reads, every second chunk of a row, evenly over the banks.
@@ -509,31 +533,29 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   if (MODE == MGS_GEMM_WGRAD && j.k == 0 && ga.accumulate) return;  // an empty group adds nothing
 
-  Operand<T, AKC> oa;
-  Operand<T, BKC> ob;
+  Operand<T, AKC, S> oa;
+  Operand<T, BKC, S> ob;
   oa.init(j.a, j.ald, j.a_bytes, j.k, 2 * (j.crow0 - (MODE == MGS_GEMM_WGRAD ? (int64_t)j.g * ga.m : 0)), 16 * F * wave,
-          32 * F * wm, wave, lane);
+          32 * F * wm, lds0, STAGE, wave, lane);
   if constexpr (EPI == EPI_GATED_FWD) {
     // B rows of a column wave: 16 F gate rows, then the same 16 F up rows; waves 2w and 2w + 1 load them
     const int half = wave & 1;
     const uint8_t* b = reinterpret_cast<const uint8_t*>(ga.b) + ((int64_t)j.g * 2 * ga.n + half * ga.n + j.ccol0) * j.bld;
-    ob.init(b, j.bld, (ga.n - j.ccol0) * j.bld, j.k, 0, 16 * F * (wave >> 1), 32 * F * wn, wave, lane);
+    ob.init(b, j.bld, (ga.n - j.ccol0) * j.bld, j.k, 0, 16 * F * (wave >> 1), 32 * F * wn, lds0 + OPB, STAGE, wave, lane);
   } else {
-    ob.init(j.b, j.bld, j.b_bytes, j.k, 2 * j.ccol0, 16 * F * wave, 32 * F * wn, wave, lane);
+    ob.init(j.b, j.bld, j.b_bytes, j.k, 2 * j.ccol0, 16 * F * wave, 32 * F * wn, lds0 + OPB, STAGE, wave, lane);
   }
   constexpr int NL = 4 * F;
-  auto begin = [&](int st) { oa.begin(st); ob.begin(st); };
-  auto load = [&](int st, int slot, int n) {
-    const uint32_t s0 = lds0 + slot * STAGE;
-    if (n < 2 * F) ob.load(st, s0 + OPB, wave, n);
-    else oa.load(st, s0, wave, n - 2 * F);
+  auto begin = [&]() { oa.begin(); ob.begin(); };
+  auto load = [&](int slot, int n) {
+    if (n < 2 * F) ob.load(slot, n);
+    else oa.load(slot, n - 2 * F);
   };
   v4i fa[2][F], fb[2][F];
   constexpr int READS = decltype(oa)::READS + decltype(ob)::READS;
   auto read = [&](int slot, int kk, int buf, int i) {
-    const lds8* s = lds + slot * STAGE;
-    if (i < decltype(ob)::READS) ob.read(s + OPB, kk, i, fb[buf], lane);
-    else oa.read(s, kk, i - decltype(ob)::READS, fa[buf], lane);
+    if (i < decltype(ob)::READS) ob.read(slot, kk, i, fb[buf]);
+    else oa.read(slot, kk, i - decltype(ob)::READS, fa[buf]);
   };
   const int nsteps = __builtin_amdgcn_readfirstlane((int)((j.k + KSTEP - 1) / KSTEP));
   // loads into a stage: LEAD of them in the step that frees it, one behind every second MFMA, the others in the
@@ -541,9 +563,9 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
   constexpr int LEAD = F == 4 ? 8 : NL;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    begin(s);
+    begin();
 #pragma unroll
-    for (int n = 0; n < (s == S - 1 ? LEAD : NL); ++n) load(s, s, n);
+    for (int n = 0; n < (s == S - 1 ? LEAD : NL); ++n) load(s, n);
   }
   // The accumulators are cleared while the loads are under way, each of its own: of equal values the compiler
   // would keep one and copy it to the others just ahead of their first MFMA, without the wait states.
@@ -563,20 +585,24 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
 #pragma unroll
   for (int i = 0; i < READS; ++i) read(0, 0, 0, i);
 
-  // the MFMAs of one substep from fragment buffer B, `behind(m)` after the m-th
+  // The MFMAs of one substep from fragment buffer `buf`, `behind(m)` after the m-th; `with(m)` says which load (into stage
+  // `to`) goes with it, -1 none.
   constexpr int PER = (READS + F * F - 1) / (F * F);  // reads behind each MFMA
-  auto substep = [&](int buf, auto&& behind) {
+  auto substep = [&](int buf, int to, auto&& with, auto&& behind) {
 #pragma unroll
     for (int fm = 0; fm < F; ++fm)
 #pragma unroll
       for (int fn = 0; fn < F; ++fn) {
+        const int m = F * fm + fn, n = with(m);
         if constexpr (F == 4) {
-          mfma_pinned(acc[fm][fn], fb[buf][fn], fa[buf][fm]);
+          if (n < 0) mfma_pinned(acc[fm][fn], fb[buf][fn], fa[buf][fm]);
+          else if (n < 2 * F) mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], ob.desc, ob.vo[n & (2 * F - 1)], ob.dst[to], (n & (2 * F - 1)) * 1024);
+          else mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], oa.desc, oa.vo[n & (2 * F - 1)], oa.dst[to], (n & (2 * F - 1)) * 1024);
         } else {
           acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[buf][fn]),
                                                                 __builtin_bit_cast(v8bf, fa[buf][fm]), acc[fm][fn], 0, 0, 0);
         }
-        behind(F * fm + fn);
+        behind(m);
         if constexpr (F == 4) __builtin_amdgcn_sched_barrier(0);
       }
   };
@@ -585,31 +611,32 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
     for (int i = m * PER; i < (m + 1) * PER; ++i)
       if (i < READS) read(slot, kk, buf, i);
   };
-  int slot = 0;
-  for (int st = 0; st < nsteps; ++st) {
-    const int prev = slot == 0 ? S - 1 : slot - 1, next = slot == S - 1 ? 0 : slot + 1;
-    substep(0, [&](int m) {
-      reads(slot, 1, 1, m);
-      if (LEAD < NL && (m & 1) && LEAD + m / 2 < NL) load(st - 1 + S, prev, LEAD + m / 2);
+  auto none = [](int) { return -1; };
+  auto step = [&](auto slot_) __attribute__((always_inline)) {
+    constexpr int slot = decltype(slot_)::value, prev = slot == 0 ? S - 1 : slot - 1, next = slot == S - 1 ? 0 : slot + 1;
+    substep(0, prev, [&](int m) { return LEAD < NL && !(m & 1) && LEAD + m / 2 < NL ? LEAD + m / 2 : -1; },
+            [&](int m) { reads(slot, 1, 1, m); });
+    substep(1, 0, none, [&](int m) {
+      reads(slot, 2, 0, m);
+      if (m == F * F - 1) begin();
     });
-    substep(1, [&](int m) { reads(slot, 2, 0, m); });
-    substep(0, [&](int m) { reads(slot, 3, 1, m); });
+    substep(0, 0, none, [&](int m) { reads(slot, 3, 1, m); });
     // from here on the next stage is loaded and this one read by every wave
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     wait_loads<(S - 2) * NL>();
     __syncthreads();
-    begin(st + S);
-    substep(1, [&](int m) {
+    substep(1, slot, [&](int m) { return F == 4 && !(m & 1) ? m / 2 : -1; }, [&](int m) {
       reads(next, 0, 0, m);
-      if constexpr (F == 4) {
-        if (m & 1) load(st + S, slot, m / 2);
-      } else if (m == 0) {
+      if (F != 4 && m == 0) {
 #pragma unroll
-        for (int n = 0; n < NL; ++n) load(st + S, slot, n);
+        for (int n = 0; n < NL; ++n) load(slot, n);
       }
     });
-    slot = next;
-  }
+  };
+  for (int st = 0; st < nsteps; st += S)
+    unrolled<S>([&](auto slot) __attribute__((always_inline)) {
+      if (st + decltype(slot)::value < nsteps) step(slot);
+    });
   __builtin_amdgcn_sched_barrier(0);
   mfma_drain();
   __builtin_amdgcn_sched_barrier(0);
