@@ -446,22 +446,23 @@ int mgs_grouped_gemm_bf16(int32_t mode, const mgs_groups* groups, int64_t m, int
  *   act      a gated kind (SWIGLU, CLAMPED_SWIGLU, GLU)
  *   x_bf16   [M x k]; w_bf16 [E x 2f x k]; bias_bf16 [E x 2f] nullable; probs [M] FP32, NULL means 1
  *   h_bf16   [M x f]
- *   pre_bf16 [M x 2f] nullable: [gate | up] rounded to BF16, which the backward takes (CLAMPED_SWIGLU: to the nearest
- *            value on the same side of the clamps, where the derivative jumps) */
+ *   pre      [M x 2f] nullable: [gate | up], which the backward takes, of pre_dtype F32 or BF16 (half the bytes, and the
+ *            gradients are of the rounded values; CLAMPED_SWIGLU: of the nearest ones on the same side of the clamps,
+ *            where the derivative jumps) */
 int mgs_grouped_gated_fwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t k, const void* x_bf16,
-                          const void* w_bf16, const void* bias_bf16, const float* probs, void* h_bf16, void* pre_bf16,
-                          void* stream);
+                          const void* w_bf16, const void* bias_bf16, const float* probs, void* h_bf16, void* pre,
+                          int32_t pre_dtype, void* stream);
 
 /* Backward of the second linear and the activation in one kernel: with da = dy_g W2_g in FP32,
  *   dpre = da * probs[row] * (d act / d gate, d act / d up) at pre, dprobs[row] = sum_j da * act(pre).
- *   dy_bf16 [M x n]; w2_bf16 [E x n x f]; pre_bf16 [M x 2f] of the forward; probs as in the forward
+ *   dy_bf16 [M x n]; w2_bf16 [E x n x f]; pre [M x 2f] of the forward, of pre_dtype; probs as in the forward
  *   dpre_bf16 [M x 2f]; the weights' and inputs' gradients are products of it (DGRAD and WGRAD above)
  *   h_bf16   [M x f] nullable: act(pre) * probs again, the second linear's input (recompute)
  *   dprobs   [M] FP32 nullable; needs the workspace, mgs_grouped_gated_bwd_workspace_bytes() bytes of
  *            scratch, caller-owned, contents undefined before and after; calls sharing it must not overlap */
 int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t n, const void* dy_bf16,
-                          const void* w2_bf16, const void* pre_bf16, const float* probs, void* dpre_bf16, void* h_bf16,
-                          float* dprobs, void* workspace, int64_t workspace_bytes, void* stream);
+                          const void* w2_bf16, const void* pre, int32_t pre_dtype, const float* probs, void* dpre_bf16,
+                          void* h_bf16, float* dprobs, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of mgs_grouped_gated_bwd's dprobs (negative MGS_ERR_* on invalid arguments). */
 int64_t mgs_grouped_gated_bwd_workspace_bytes(const mgs_groups* groups, int64_t f);

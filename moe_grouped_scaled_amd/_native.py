@@ -100,8 +100,8 @@ def _load():
         "mgs_moe_combine": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, vp, vp, i64, vp]),
         "mgs_moe_combine_bwd": (ctypes.c_int, [i64, i32, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
         "mgs_grouped_gemm_bf16": (ctypes.c_int, [i32, pgr, i64, i64, i64, vp, vp, vp, i32, vp, i32, vp]),
-        "mgs_grouped_gated_fwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp]),
-        "mgs_grouped_gated_bwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "mgs_grouped_gated_fwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, vp, vp, vp, ctypes.c_int32, vp]),
+        "mgs_grouped_gated_bwd": (ctypes.c_int, [pact, pgr, i64, i64, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, i64, vp]),
         "mgs_grouped_gated_bwd_workspace_bytes": (i64, [pgr, i64]),
         "mgs_w4_nbytes": (i64, [i32, i64, i64, i32, i32]),
         "mgs_w4_pack": (ctypes.c_int, [i32, i64, i64, i32, vp, vp, vp, vp, vp]),

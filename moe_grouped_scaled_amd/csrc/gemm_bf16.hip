@@ -55,8 +55,9 @@ struct BfArgs {
   ActArgs act;
   float lim_in, lim_out;  // clamped SwiGLU: the largest BF16 value at most the limit, the smallest above it
   const float* probs;
-  uint16_t* pre_out;      // gated forward: [M x 2n], nullable
-  const uint16_t* pre;    // gated backward: [M x 2n]
+  void* pre_out;          // gated forward: [M x 2n], nullable
+  const void* pre;        // gated backward: [M x 2n]
+  int pre_f32;            // type of either: FP32, or BF16
   uint16_t* h_out;        // gated backward: [M x n], nullable
   float* dp_part;         // gated backward: [M x dp_ld] partial sums of dprobs, nullable
   int64_t dp_ld;
@@ -188,6 +189,11 @@ __device__ __forceinline__ void st16(void* p, v4u v) {
   if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(p));
   else *reinterpret_cast<v4u*>(p) = v;
   asm volatile("s_nop 1" ::"v"(v));
+}
+template <bool NT>
+__device__ __forceinline__ void st_f32x8(float* p, const float (&v)[8]) {
+  st16<NT>(p, v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+  st16<NT>(p + 4, v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
 }
 template <bool NT>
 __device__ __forceinline__ void st_bf16x8(uint16_t* p, const float (&v)[8]) {
@@ -348,6 +354,26 @@ __device__ __forceinline__ void add_bf16x8(float (&v)[8], const uint4& w) {
   v[4] += bf16lo(w.z); v[5] += bf16hi(w.z); v[6] += bf16lo(w.w); v[7] += bf16hi(w.w);
 }
 
+// [gate | up] of the wave's staged rows in FP32, with their bias: one 16-byte chunk a lane, so that a store writes whole
+// lines (with the eight columns a lane of the rows below, two stores write every second chunk each).
+template <int F>
+__device__ __forceinline__ void pre_f32_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
+  constexpr int W = 16 * F, LPR = 2 * W / 4, RPP = 64 / LPR;
+  const int lr = lane / LPR, c = lane % LPR, half = c / (W / 4), col = wn * W + 4 * (c % (W / 4));
+  if (col >= j.cols) return;
+  const int64_t gc = half * ga.n + j.ccol0 + col;
+  uint2 b = make_uint2(0, 0);
+  if (ga.bias) b = *reinterpret_cast<const uint2*>(ga.bias + (int64_t)j.g * 2 * ga.n + gc);
+  const v4f add = {bf16lo(b.x), bf16hi(b.x), bf16lo(b.y), bf16hi(b.y)};
+#pragma unroll 2
+  for (int i = 0; i < 32 / RPP; ++i) {
+    const int row = RPP * i + lr;
+    if (row0 + row >= j.rows) continue;
+    const v4f v = *reinterpret_cast<const lds_f4*>(staged<F>(buf, row, c)) + add;
+    st16<F == 4>(static_cast<float*>(ga.pre_out) + (j.crow0 + row0 + row) * 2 * ga.n + gc, __builtin_bit_cast(v4u, v));
+  }
+}
+
 // The gated forward: a wave's staged rows are 16 F gate columns and the same up columns.
 template <int KIND, int F>
 __device__ __forceinline__ void gated_fwd_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
@@ -376,7 +402,7 @@ __device__ __forceinline__ void gated_fwd_rows(const Job& j, const BfArgs& ga, l
 #pragma unroll
     for (int t = 0; t < 8; ++t) h[t] = act_gated<KIND>(v[t], u[t], ga.act) * s;
     st_bf16x8<NT>(static_cast<uint16_t*>(ga.c) + gr * ga.n + gc, h);
-    if (ga.pre_out) {
+    if (ga.pre_out && !ga.pre_f32) {
       if constexpr (KIND == MGS_ACT_CLAMPED_SWIGLU) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
@@ -384,41 +410,74 @@ __device__ __forceinline__ void gated_fwd_rows(const Job& j, const BfArgs& ga, l
           u[t] = same_side(u[t], ga);
         }
       }
-      st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + gc, v);
-      st_bf16x8<NT>(ga.pre_out + gr * 2 * ga.n + ga.n + gc, u);
+      uint16_t* p = static_cast<uint16_t*>(ga.pre_out) + gr * 2 * ga.n + gc;
+      st_bf16x8<NT>(p, v);
+      st_bf16x8<NT>(p + ga.n, u);
     }
   }
 }
 
 // The gated backward: da beside what the forward saved of the same eight columns, which is loaded one pass ahead.
-template <int KIND, int F>
+template <bool P32>
+struct Saved;  // of eight columns: gate, up, and the row's scale
+template <>
+struct Saved<false> {
+  uint4 g, u;
+  float s;
+  __device__ __forceinline__ void load(const void* p, int64_t at, int64_t n) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    g = *reinterpret_cast<const uint4*>(q);
+    u = *reinterpret_cast<const uint4*>(q + n);
+  }
+  __device__ __forceinline__ void values(float (&gate)[8], float (&up)[8]) const {
+    unpack8(g, gate);
+    unpack8(u, up);
+  }
+};
+template <>
+struct Saved<true> {
+  float4 g0, g1, u0, u1;
+  float s;
+  __device__ __forceinline__ void load(const void* p, int64_t at, int64_t n) {
+    const float* q = static_cast<const float*>(p) + at;
+    g0 = *reinterpret_cast<const float4*>(q);
+    g1 = *reinterpret_cast<const float4*>(q + 4);
+    u0 = *reinterpret_cast<const float4*>(q + n);
+    u1 = *reinterpret_cast<const float4*>(q + n + 4);
+  }
+  __device__ __forceinline__ void values(float (&gate)[8], float (&up)[8]) const {
+    gate[0] = g0.x; gate[1] = g0.y; gate[2] = g0.z; gate[3] = g0.w;
+    gate[4] = g1.x; gate[5] = g1.y; gate[6] = g1.z; gate[7] = g1.w;
+    up[0] = u0.x; up[1] = u0.y; up[2] = u0.z; up[3] = u0.w;
+    up[4] = u1.x; up[5] = u1.y; up[6] = u1.z; up[7] = u1.w;
+  }
+};
+
+template <int KIND, bool P32, int F>
 __device__ __forceinline__ void gated_bwd_rows(const Job& j, const BfArgs& ga, lds8* buf, int row0, int wn, int lane) {
   constexpr bool NT = F == 4;
   constexpr int W = 32 * F, LPR = W / 8, RPP = 64 / LPR;
   const int lr = lane / LPR, lc = lane % LPR;
   const bool cok = wn * W + 8 * lc < j.cols;
   const int64_t gc = j.ccol0 + wn * W + 8 * lc, ld = 2 * ga.n, gr0 = j.crow0 + row0;
-  struct Saved { uint4 g, u; float s; };
   auto saved = [&](int row) {
-    Saved x{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), 1.0f};
+    Saved<P32> x{};
+    x.s = 1.0f;
     if (cok && row < 32 && row0 + row < j.rows) {
-      const uint16_t* p = ga.pre + (gr0 + row) * ld + gc;
-      x.g = *reinterpret_cast<const uint4*>(p);
-      x.u = *reinterpret_cast<const uint4*>(p + ga.n);
+      x.load(ga.pre, (gr0 + row) * ld + gc, ga.n);
       if (ga.probs) x.s = ga.probs[gr0 + row];
     }
     return x;
   };
-  Saved next = saved(lr);
+  Saved<P32> next = saved(lr);
 #pragma unroll 2
   for (int i = 0; i < 32 / RPP; ++i) {
     const int row = RPP * i + lr;
-    const Saved now = next;
+    const Saved<P32> now = next;
     next = saved(row + RPP);
     float v[8], g[8], u[8], dg[8], du[8], h[8], dp = 0.0f;
     staged8<F>(buf, row, 8 * lc, v);
-    unpack8(now.g, g);
-    unpack8(now.u, u);
+    now.values(g, u);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       float a, bg, bu;
@@ -472,8 +531,7 @@ __device__ __forceinline__ void plain_rows(const Job& j, const BfArgs& ga, lds8*
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
         v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
       }
-      st16<NT>(c, v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-      st16<NT>(c + 4, v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
+      st_f32x8<NT>(c, v);
     } else {
       st_bf16x8<NT>(static_cast<uint16_t*>(ga.c) + at, v);
     }
@@ -488,13 +546,19 @@ __device__ __forceinline__ void epilogue(const Job& j, const BfArgs& ga, v16f (&
     if (row0 >= j.rows) return;
     stage_f32<F>(acc[fm], buf, lane);
     if constexpr (EPI == EPI_GATED_FWD) {
+      if (ga.pre_out && ga.pre_f32) pre_f32_rows<F>(j, ga, buf, row0, wn, lane);
       if (ga.act.kind == MGS_ACT_SWIGLU) gated_fwd_rows<MGS_ACT_SWIGLU, F>(j, ga, buf, row0, wn, lane);
       else if (ga.act.kind == MGS_ACT_GLU) gated_fwd_rows<MGS_ACT_GLU, F>(j, ga, buf, row0, wn, lane);
       else gated_fwd_rows<MGS_ACT_CLAMPED_SWIGLU, F>(j, ga, buf, row0, wn, lane);
     } else if constexpr (EPI == EPI_GATED_BWD) {
-      if (ga.act.kind == MGS_ACT_SWIGLU) gated_bwd_rows<MGS_ACT_SWIGLU, F>(j, ga, buf, row0, wn, lane);
-      else if (ga.act.kind == MGS_ACT_GLU) gated_bwd_rows<MGS_ACT_GLU, F>(j, ga, buf, row0, wn, lane);
-      else gated_bwd_rows<MGS_ACT_CLAMPED_SWIGLU, F>(j, ga, buf, row0, wn, lane);
+      auto rows = [&](auto p32) __attribute__((always_inline)) {
+        constexpr bool P32 = decltype(p32)::value;
+        if (ga.act.kind == MGS_ACT_SWIGLU) gated_bwd_rows<MGS_ACT_SWIGLU, P32, F>(j, ga, buf, row0, wn, lane);
+        else if (ga.act.kind == MGS_ACT_GLU) gated_bwd_rows<MGS_ACT_GLU, P32, F>(j, ga, buf, row0, wn, lane);
+        else gated_bwd_rows<MGS_ACT_CLAMPED_SWIGLU, P32, F>(j, ga, buf, row0, wn, lane);
+      };
+      if (ga.pre_f32) rows(std::true_type{});
+      else rows(std::false_type{});
     } else {
       if (ga.c_f32) plain_rows<true, F>(j, ga, buf, row0, wn, lane);
       else plain_rows<false, F>(j, ga, buf, row0, wn, lane);
@@ -765,7 +829,7 @@ __global__ __launch_bounds__(64 * WAVES) void rows_bf16_kernel(BfArgs ga, GroupT
         if (ga.c_f32) {
           float* c = reinterpret_cast<float*>(ga.c) + gr * ga.n + gc;
           if (ga.accumulate) v += *reinterpret_cast<const v4f*>(c);
-          st16<false>(c, v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+          st16<false>(c, __builtin_bit_cast(v4u, v));
         } else {
           store(reinterpret_cast<uint16_t*>(ga.c) + gr * ga.n + gc, v);
         }
@@ -779,7 +843,11 @@ __global__ __launch_bounds__(64 * WAVES) void rows_bf16_kernel(BfArgs ga, GroupT
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = act_gated_of(ga.act.kind, v[e], u[e], ga.act) * s;
         store(reinterpret_cast<uint16_t*>(ga.c) + gr * ga.n + gc, h);
-        if (ga.pre_out) {
+        if (ga.pre_out && ga.pre_f32) {
+          float* p = static_cast<float*>(ga.pre_out) + gr * nb + gc;
+          st16<false>(p, __builtin_bit_cast(v4u, v));
+          st16<false>(p + ga.n, __builtin_bit_cast(v4u, u));
+        } else if (ga.pre_out) {
           if (ga.act.kind == MGS_ACT_CLAMPED_SWIGLU) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -787,8 +855,9 @@ __global__ __launch_bounds__(64 * WAVES) void rows_bf16_kernel(BfArgs ga, GroupT
               u[e] = same_side(u[e], ga);
             }
           }
-          store(ga.pre_out + gr * nb + gc, v);
-          store(ga.pre_out + gr * nb + ga.n + gc, u);
+          uint16_t* p = static_cast<uint16_t*>(ga.pre_out) + gr * nb + gc;
+          store(p, v);
+          store(p + ga.n, u);
         }
       }
     }
@@ -1003,6 +1072,11 @@ int check_gated(const mgs_act_params* act, ActArgs* out) {
   return MGS_OK;
 }
 
+int check_pre_dtype(int32_t dtype) {
+  if (dtype != MGS_DTYPE_BF16 && dtype != MGS_DTYPE_F32) return fail(MGS_ERR_INVALID_ARG, "unknown type of pre %d", dtype);
+  return MGS_OK;
+}
+
 int64_t dp_columns(int64_t f) { return 2 * ((f + 63) / 64); }  // partial sums of a row (64-wide tiles have the most)
 
 }  // namespace
@@ -1050,8 +1124,8 @@ int mgs_grouped_gemm_bf16(int32_t mode, const mgs_groups* groups, int64_t m, int
 }
 
 int mgs_grouped_gated_fwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t k, const void* x_bf16,
-                          const void* w_bf16, const void* bias_bf16, const float* probs, void* h_bf16, void* pre_bf16,
-                          void* stream) {
+                          const void* w_bf16, const void* bias_bf16, const float* probs, void* h_bf16, void* pre,
+                          int32_t pre_dtype, void* stream) {
   BfArgs ga{};
   int rc = check_gated(act, &ga.act);
   if (rc) return rc;
@@ -1059,10 +1133,11 @@ int mgs_grouped_gated_fwd(const mgs_act_params* act, const mgs_groups* groups, i
   int64_t rows = 0;
   if ((rc = build_groups(groups, &gt, &rows))) return rc;
   if ((rc = check_bf16_width(f, "f")) || (rc = check_bf16_width(k, "k"))) return rc;
+  if (pre && (rc = check_pre_dtype(pre_dtype))) return rc;
   if (rows > 0 && (!x_bf16 || !w_bf16 || !h_bf16)) return fail(MGS_ERR_INVALID_ARG, "x, w or h is NULL");
   const int64_t e = gt.num_groups;
   const Range rx{"x", x_bf16, 2 * rows * k}, rw{"w", w_bf16, 4 * e * f * k}, rbias{"bias", bias_bf16, 4 * e * f},
-      rp{"probs", probs, 4 * rows}, rh{"h", h_bf16, 2 * rows * f}, rpre{"pre", pre_bf16, 4 * rows * f};
+      rp{"probs", probs, 4 * rows}, rh{"h", h_bf16, 2 * rows * f}, rpre{"pre", pre, (pre_dtype == MGS_DTYPE_F32 ? 8 : 4) * rows * f};
   if ((rc = check_aligned({rx, rw, rbias, rh, rpre}, 16)) || (rc = check_aligned({rp}, 4))) return rc;
   if ((rc = check_ranges({rh, rpre}, {rx, rw, rbias, rp}))) return rc;
   if (rows == 0) return ok();
@@ -1080,7 +1155,8 @@ int mgs_grouped_gated_fwd(const mgs_act_params* act, const mgs_groups* groups, i
   ga.c = h_bf16;
   ga.bias = static_cast<const uint16_t*>(bias_bf16);
   ga.probs = probs;
-  ga.pre_out = static_cast<uint16_t*>(pre_bf16);
+  ga.pre_out = pre;
+  ga.pre_f32 = pre_dtype == MGS_DTYPE_F32;
   return launch(ga, EPI_GATED_FWD, gt, dev_gemm_table(groups), static_cast<hipStream_t>(stream));
 }
 
@@ -1095,8 +1171,8 @@ int64_t mgs_grouped_gated_bwd_workspace_bytes(const mgs_groups* groups, int64_t 
 }
 
 int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, int64_t f, int64_t n, const void* dy_bf16,
-                          const void* w2_bf16, const void* pre_bf16, const float* probs, void* dpre_bf16, void* h_bf16,
-                          float* dprobs, void* workspace, int64_t workspace_bytes, void* stream) {
+                          const void* w2_bf16, const void* pre, int32_t pre_dtype, const float* probs, void* dpre_bf16,
+                          void* h_bf16, float* dprobs, void* workspace, int64_t workspace_bytes, void* stream) {
   BfArgs ga{};
   int rc = check_gated(act, &ga.act);
   if (rc) return rc;
@@ -1104,12 +1180,13 @@ int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, i
   int64_t rows = 0;
   if ((rc = build_groups(groups, &gt, &rows))) return rc;
   if ((rc = check_bf16_width(f, "f")) || (rc = check_bf16_width(n, "n"))) return rc;
-  if (rows > 0 && (!dy_bf16 || !w2_bf16 || !pre_bf16 || !dpre_bf16)) return fail(MGS_ERR_INVALID_ARG, "dy, w2, pre or dpre is NULL");
+  if ((rc = check_pre_dtype(pre_dtype))) return rc;
+  if (rows > 0 && (!dy_bf16 || !w2_bf16 || !pre || !dpre_bf16)) return fail(MGS_ERR_INVALID_ARG, "dy, w2, pre or dpre is NULL");
   const int64_t e = gt.num_groups, need = dprobs ? 4 * rows * dp_columns(f) : 0;
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(MGS_ERR_INVALID_ARG, "dprobs needs a workspace of %lld bytes (got %lld%s)", (long long)need,
                 (long long)workspace_bytes, workspace ? "" : ", NULL");
-  const Range rdy{"dy", dy_bf16, 2 * rows * n}, rw{"w2", w2_bf16, 2 * e * n * f}, rpre{"pre", pre_bf16, 4 * rows * f},
+  const Range rdy{"dy", dy_bf16, 2 * rows * n}, rw{"w2", w2_bf16, 2 * e * n * f}, rpre{"pre", pre, (pre_dtype == MGS_DTYPE_F32 ? 8 : 4) * rows * f},
       rp{"probs", probs, 4 * rows}, rd{"dpre", dpre_bf16, 4 * rows * f}, rh{"h", h_bf16, 2 * rows * f},
       rdp{"dprobs", dprobs, 4 * rows}, rws{"the workspace", need ? workspace : nullptr, need};
   if ((rc = check_aligned({rdy, rw, rpre, rd, rh}, 16)) || (rc = check_aligned({rp, rdp, rws}, 4))) return rc;
@@ -1120,7 +1197,8 @@ int mgs_grouped_gated_bwd(const mgs_act_params* act, const mgs_groups* groups, i
   ga.a = static_cast<const uint16_t*>(dy_bf16);
   ga.b = static_cast<const uint16_t*>(w2_bf16);
   ga.c = dpre_bf16;
-  ga.pre = static_cast<const uint16_t*>(pre_bf16);
+  ga.pre = pre;
+  ga.pre_f32 = pre_dtype == MGS_DTYPE_F32;
   ga.h_out = static_cast<uint16_t*>(h_bf16);
   ga.probs = probs;
   const hipStream_t st = static_cast<hipStream_t>(stream);

@@ -94,8 +94,8 @@ def grouped_gemm_bf16(mode, split_sizes, a, b, c=None, bias=None, accumulate=Fal
 
 def grouped_gated_fwd(act, split_sizes, x, w, bias=None, probs=None, h=None, pre=None, stream=None):
     """h = act(gate, up) * probs with [gate | up] = x w_g^T + bias in FP32: x [M, k], w [E, 2f, k], bias [E, 2f], probs
-    [M] FP32 (1 when None).  `act`: "swiglu", "clamped_swiglu", "glu" or `act_params(...)` of one.  `pre` [M, 2f]
-    receives [gate | up] in BF16 for the backward.  Returns h [M, f]."""
+    [M] FP32 (1 when None).  `act`: "swiglu", "clamped_swiglu", "glu" or `act_params(...)` of one.  `pre` [M, 2f],
+    FP32 or BF16, receives [gate | up] for the backward.  Returns h [M, f]."""
     if stream is not None:
         return _on_stream(stream, x, grouped_gated_fwd, act, split_sizes, x, w, bias, probs, h, pre)
     act = _gated_act(act)
@@ -111,7 +111,7 @@ def grouped_gated_fwd(act, split_sizes, x, w, bias=None, probs=None, h=None, pre
     h = _given("h", h, _BF16, (rows, f2 // 2), dev)
     _call(dev, N.LIB.mgs_grouped_gated_fwd, act, g.ref, f2 // 2, k, x.data_ptr(), w.data_ptr(),
           _maybe("bias", bias, _BF16, (e, f2), dev), _maybe("probs", probs, _F32, (rows,), dev), h.data_ptr(),
-          _maybe("pre", pre, _BF16, (rows, f2), dev))
+          _maybe("pre", pre, _OUT, (rows, f2), dev), N.DTYPE[torch.float32 if pre is None else pre.dtype])
     return h
 
 
@@ -136,7 +136,7 @@ def grouped_gated_bwd(act, split_sizes, dy, w2, pre, probs=None, dpre=None, h=No
     e, f = w2.shape[0], w2.shape[2]
     if w2.shape[1] != n:
         _fail("w2 has %d rows an expert, dy is %d wide", w2.shape[1], n)
-    _check("pre", pre, _BF16, 2, dev, shape=(rows, 2 * f))
+    _check("pre", pre, _OUT, 2, dev, shape=(rows, 2 * f))
     g = _groups(split_sizes, rows, e, dev)
     dpre = _given("dpre", dpre, _BF16, (rows, 2 * f), dev)
     dp = _maybe("dprobs", dprobs, _F32, (rows,), dev)
@@ -145,7 +145,7 @@ def grouped_gated_bwd(act, split_sizes, dy, w2, pre, probs=None, dpre=None, h=No
         if workspace is None:
             workspace = torch.empty(grouped_gated_bwd_workspace_bytes(split_sizes, f), dtype=torch.uint8, device=dev)
         ws, wb = _check("workspace", workspace, (torch.uint8,), 1, dev).data_ptr(), workspace.numel()
-    _call(dev, N.LIB.mgs_grouped_gated_bwd, act, g.ref, f, n, dy.data_ptr(), w2.data_ptr(), pre.data_ptr(),
+    _call(dev, N.LIB.mgs_grouped_gated_bwd, act, g.ref, f, n, dy.data_ptr(), w2.data_ptr(), pre.data_ptr(), N.DTYPE[pre.dtype],
           _maybe("probs", probs, _F32, (rows,), dev), dpre.data_ptr(), _maybe("h", h, _BF16, (rows, f), dev), dp, ws, wb)
     return dpre
 
@@ -157,17 +157,21 @@ class GatedMLP:
     forward(x1 [M, H], probs [M] FP32 or None, split_sizes) -> y2 [M, H]; backward(dy2) -> dx1 and dprobs and, unless
     `delay_wgrad`, dw1, dw2 (of `dw_dtype`, FP32 by default) and db1, db2 (FP32); each gradient is
     requested by grad_x1, grad_probs, grad_fc1, grad_fc2, and what only an unrequested one needs is neither
-    computed nor kept.  The forward keeps [gate | up] in BF16, and with `recompute` regenerates the second linear's
-    input from it in the backward instead of keeping that too; the regenerated rows then differ from the
-    forward's, which come from the FP32 sums, by the rounding of [gate | up].  Rows are one captured step's own:
+    computed nor kept.  The forward keeps [gate | up] in `save_dtype`: FP32, or BF16 for half the memory (the
+    gradients are then those at the rounded values, and carry that rounding's error beside their own), and with `recompute`
+    regenerates the second linear's input from it in the backward instead of keeping that too (from BF16, the regenerated
+    rows differ from the forward's by the rounding of [gate | up]).  Rows are one captured step's own:
     every forward allocates its outputs."""
 
     def __init__(self, kind, w1, w2, b1=None, b2=None, recompute=False, delay_wgrad=False, limit=7.0, alpha=1.0, beta=0.0,
-                 grad_x1=True, grad_probs=True, grad_fc1=True, grad_fc2=True, dw_dtype=torch.float32):
+                 grad_x1=True, grad_probs=True, grad_fc1=True, grad_fc2=True, dw_dtype=torch.float32,
+                 save_dtype=torch.float32):
         if kind not in GATED:
             _fail("kind must be one of %s, not %r", ", ".join(GATED), kind)
         if dw_dtype not in _OUT:
             _fail("dw_dtype must be torch.bfloat16 or torch.float32, not %s", dw_dtype)
+        if save_dtype not in _OUT:
+            _fail("save_dtype must be torch.bfloat16 or torch.float32, not %s", save_dtype)
         _check("w1", w1, _BF16, 3)
         self.e, self.f_in, self.h = w1.shape
         if self.f_in % 2:
@@ -177,7 +181,7 @@ class GatedMLP:
         _check("w2", w2, _BF16, 3, dev, shape=(self.e, self.h, self.f))
         _maybe("b1", b1, _BF16, (self.e, self.f_in), dev)
         _maybe("b2", b2, _BF16, (self.e, self.h), dev)
-        self.kind, self.fmt, self.dw_dtype = kind, "bf16", dw_dtype
+        self.kind, self.fmt, self.dw_dtype, self.save_dtype = kind, "bf16", dw_dtype, save_dtype
         self.w1, self.w2, self.b1, self.b2 = w1, w2, b1, b2
         self.recompute, self.delay_wgrad = bool(recompute), bool(delay_wgrad)
         self.grad_x1, self.grad_probs, self.grad_fc1, self.grad_fc2 = grad_x1, grad_probs, grad_fc1, grad_fc2
@@ -196,7 +200,7 @@ class GatedMLP:
             splits = [int(s) for s in splits]
         with torch.cuda.device(x1.device):
             keep_pre = self.grad_below_fc2 or (self.grad_fc2 and self.recompute)
-            pre = torch.empty((x1.shape[0], self.f_in), dtype=torch.bfloat16, device=x1.device) if keep_pre else None
+            pre = torch.empty((x1.shape[0], self.f_in), dtype=self.save_dtype, device=x1.device) if keep_pre else None
             a = grouped_gated_fwd(self.act, splits, x1, self.w1, self.b1, probs, pre=pre)
             y2 = grouped_gemm_bf16("fprop", splits, a, self.w2, bias=self.b2)
         self.ctx = dict(splits=splits, probs=probs, pre=pre, x1=x1 if self.grad_fc1 else None,

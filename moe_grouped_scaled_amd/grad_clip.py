@@ -1,7 +1,7 @@
 """The global norm of many gradients, and clipping by it.
 
 Both enqueue the library's kernels on the tensors' device, on its current stream (or on `stream`, as in `moe`), and
-return the norm as an FP32 tensor [1] on that device: nothing synchronises, and a captured step clips by each
+return the norm as an FP32 scalar tensor on that device: nothing synchronises, and a captured step clips by each
 replay's own norm.  The addresses of the gradients travel with the call.
 """
 
@@ -61,7 +61,7 @@ def _run(grads, clip, max_norm, eps, out, workspace, norm):
     elif workspace.device != dev or not workspace.is_contiguous():
         _fail("workspace must be contiguous and on %s", dev)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = torch.empty((), dtype=torch.float32, device=dev)
     elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != dev:
         _fail("norm must be one FP32 element on %s", dev)
     _call(dev, N.LIB.mgs_grad_norm, len(grads), at, norm.data_ptr(), workspace.data_ptr(),

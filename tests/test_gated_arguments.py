@@ -41,11 +41,11 @@ def test_gemm_without_rows():
     assert gemm(splits=(0, 0), m=0, a=None, b=None, c=None)[0] == 0
 
 
-def fwd(kind="swiglu", splits=(4,), f=64, k=64, x=FAKE, w=FAKE << 4, bias=None, probs=None, h=FAKE << 8, pre=None, **kw):
+def fwd(kind="swiglu", splits=(4,), f=64, k=64, x=FAKE, w=FAKE << 4, bias=None, probs=None, h=FAKE << 8, pre=None, pdt=1, **kw):
     import ctypes
     from moe_grouped_scaled_amd import _native as N
     act = None if kind is None else ctypes.byref(N.act_params(kind, **kw))
-    return _call("mgs_grouped_gated_fwd", act, _groups(list(splits)), f, k, x, w, bias, probs, h, pre, 0)
+    return _call("mgs_grouped_gated_fwd", act, _groups(list(splits)), f, k, x, w, bias, probs, h, pre, pdt, 0)
 
 
 @pytest.mark.parametrize("change,code,match", [
@@ -54,6 +54,7 @@ def fwd(kind="swiglu", splits=(4,), f=64, k=64, x=FAKE, w=FAKE << 4, bias=None, 
     (dict(x=None), -1, "x, w or h"), (dict(w=None), -1, "x, w or h"), (dict(h=None), -1, "x, w or h"),
     (dict(x=FAKE + 2), -1, "x must be 16-byte"), (dict(probs=FAKE + 2), -1, "probs must be 4-byte"),
     (dict(pre=FAKE << 8), -1, "overlap pre"), (dict(pre=FAKE + 256), -1, "overlap x"), (dict(probs=(FAKE << 8) + 508), -1, "overlap probs"),
+    (dict(pre=FAKE << 9, pdt=2), -1, "type of pre"), (dict(pre=FAKE - 1040, pdt=1), -1, "overlap x"),
 ])
 def test_gated_forward_refusals(change, code, match):
     rc, msg = fwd(**change)
@@ -61,10 +62,10 @@ def test_gated_forward_refusals(change, code, match):
 
 
 def bwd(kind="swiglu", splits=(4,), f=64, n=64, dy=FAKE, w2=FAKE << 4, pre=FAKE << 8, probs=None, dpre=FAKE << 12, h=None, dp=None,
-        ws=None, wb=0):
+        ws=None, wb=0, pdt=0):
     import ctypes
     from moe_grouped_scaled_amd import _native as N
-    return _call("mgs_grouped_gated_bwd", ctypes.byref(N.act_params(kind)), _groups(list(splits)), f, n, dy, w2, pre, probs,
+    return _call("mgs_grouped_gated_bwd", ctypes.byref(N.act_params(kind)), _groups(list(splits)), f, n, dy, w2, pre, pdt, probs,
                  dpre, h, dp, ws, wb, 0)
 
 
@@ -73,6 +74,7 @@ def bwd(kind="swiglu", splits=(4,), f=64, n=64, dy=FAKE, w2=FAKE << 4, pre=FAKE 
     (dict(pre=None), -1, "dpre is NULL"), (dict(dpre=None), -1, "dpre is NULL"), (dict(dp=FAKE << 2), -1, "workspace of 32 bytes"),
     (dict(dp=FAKE << 2, ws=FAKE << 3, wb=31), -1, "got 31"), (dict(dpre=FAKE << 8), -1, "overlap pre"),
     (dict(h=(FAKE << 12) + 1008), -1, "dpre must not be or overlap h"), (dict(dp=FAKE << 2, ws=FAKE << 2, wb=32), -1, "overlap the workspace"),
+    (dict(pdt=3), -1, "type of pre"), (dict(dpre=(FAKE << 8) + 1024, pdt=1), -1, "overlap pre"),
 ])
 def test_gated_backward_refusals(change, code, match):
     rc, msg = bwd(**change)

@@ -179,10 +179,13 @@ def test_other_groups_do_not_reach_a_group(M, mode, n, k, splits):
 
 
 def check_pre(out, pre, dpre, kind, f):
-    """[gate | up] in BF16: to nearest, or for the clamped kind to the same side of the clamps.  Then a value within half a
+    """[gate | up]: in FP32 the sums themselves; in BF16 to nearest, or for the clamped kind to the same side of the clamps.  Then a value within half a
     step of a limit moves by up to the whole step to the first one on its side, 2 x 2^-8 of it.  Sides are compared
     where the sum's own error does not reach the limit."""
     import torch
+    if out.dtype == torch.float32:
+        check(out, pre, dpre, "pre")
+        return
     u = torch.full_like(pre, UBF)
     if kind == "clamped_swiglu":
         d = (pre.abs() - LIMIT).abs()
@@ -232,11 +235,12 @@ def test_gated_forward(M, kind, split, f, k):
     for bias, probs in ((True, True), (False, False)):
         x, w, b, p = gated_case(kind, splits, f, k, seed=f, bias=bias, probs=probs)
         ref, tol, pre, dpre = gated64(kind, splits, x, w, b, p)
-        out = torch.full((sum(splits), 2 * f), math.nan, dtype=torch.bfloat16, device="cuda")
         xg, wg, bg, pg = cuda(x, w, b, p)
-        h = M.grouped_gated_fwd(act_of(kind), splits, xg, wg, bg, pg, pre=out)
-        check(h, ref, tol + UBF * ref.abs(), "h")
-        check_pre(out, pre, dpre, kind, f)
+        for dt in (torch.bfloat16, torch.float32):
+            out = torch.full((sum(splits), 2 * f), math.nan, dtype=dt, device="cuda")
+            h = M.grouped_gated_fwd(act_of(kind), splits, xg, wg, bg, pg, pre=out)
+            check(h, ref, tol + UBF * ref.abs(), "h")
+            check_pre(out, pre, dpre, kind, f)
         assert torch.equal(h, M.grouped_gated_fwd(act_of(kind), splits, xg, wg, bg, pg))
 
 
@@ -246,18 +250,19 @@ def test_gated_forward_on_larger_tiles(M, splits, f, k):
     x, w, b, p = gated_case("swiglu", splits, f, k, seed=7)
     ref, tol, pre, dpre = gated64("swiglu", splits, x, w, b, p)
     xg, wg, bg, pg = cuda(x, w, b, p)
-    out = torch.empty((sum(splits), 2 * f), dtype=torch.bfloat16, device="cuda")
-    h = M.grouped_gated_fwd(act_of("swiglu"), splits, xg, wg, bg, pg, pre=out)
-    check(h, ref, tol + UBF * ref.abs(), "h")
-    check_pre(out, pre, dpre, "swiglu", f)
+    for dt in (torch.bfloat16, torch.float32):
+        out = torch.empty((sum(splits), 2 * f), dtype=dt, device="cuda")
+        h = M.grouped_gated_fwd(act_of("swiglu"), splits, xg, wg, bg, pg, pre=out)
+        check(h, ref, tol + UBF * ref.abs(), "h")
+        check_pre(out, pre, dpre, "swiglu", f)
 
 
-def check_backward(M, kind, splits, f, n, seed, probs):
+def check_backward(M, kind, splits, f, n, seed, probs, pre_dtype):
     import torch
     gen = torch.Generator().manual_seed(seed)
     m, e = sum(splits), len(splits)
     dy, w2 = normal(gen, m, n), normal(gen, e, n, f, std=n ** -0.5)
-    pre = normal(gen, m, 2 * f, std=1.5)
+    pre = (torch.randn(m, 2 * f, generator=gen) * 1.5).to(pre_dtype)
     p = torch.rand(m, generator=gen) if probs else None
     da, mag = product64("dgrad", splits, dy, w2)
     d = (n + 2) * U32 * mag
@@ -280,13 +285,16 @@ def check_backward(M, kind, splits, f, n, seed, probs):
 @pytest.mark.parametrize("f,n", [(8, 8), (72, 136), (264, 200)])
 @pytest.mark.parametrize("split", sorted(SPLITS))
 def test_gated_backward(M, kind, split, f, n):
-    for probs in (True, False):
-        check_backward(M, kind, SPLITS[split], f, n, seed=n, probs=probs)
+    import torch
+    for probs, dt in ((True, torch.bfloat16), (True, torch.float32), (False, torch.float32)):
+        check_backward(M, kind, SPLITS[split], f, n, seed=n, probs=probs, pre_dtype=dt)
 
 
 @pytest.mark.parametrize("splits,f,n", [([100, 300, 0, 77], 6400, 40), ([1000, 500], 8192 - 8, 200)])
 def test_gated_backward_on_larger_tiles(M, splits, f, n):
-    check_backward(M, "swiglu", splits, f, n, seed=9, probs=True)
+    import torch
+    for dt in (torch.bfloat16, torch.float32):
+        check_backward(M, "swiglu", splits, f, n, seed=9, probs=True, pre_dtype=dt)
 
 
 @pytest.mark.parametrize("kind", KINDS)
