@@ -219,10 +219,10 @@ __device__ __forceinline__ float same_side_gate(float v, const BfArgs& ga) {
 }
 
 // One operand of the kernel: the loads of its part of a stage, and its fragments.  T: its rows (outputs) of
-// the tile, F = T / 64 fragments a wave; KC: k-contiguous; S stages.  Everything that a step's loads and reads need is
+// the tile, F = T / 64 fragments a wave, STEP rows apart; KC: k-contiguous; S stages.  Everything that a step's loads and reads need is
 // in registers before the loop (lane offsets, LDS addresses of every stage), so that behind an MFMA stand one or two
 // instructions: the wave is alone on its SIMD, and what does not fit behind its MFMAs holds them up.
-template <int T, bool KC, int S>
+template <int T, bool KC, int S, int STEP>
 struct Operand {
   static constexpr int F = T / 64, PITCH = 2 * T;   // bytes of a stage row (not KC)
   static constexpr int LOADS = 2 * F;               // per wave and step
@@ -271,7 +271,7 @@ struct Operand {
         if constexpr (KC) {
           rd[s][i] = lds + s * stage + (uint32_t)(w0 + r32) * 128 + (((2 * i + h32) ^ ((r32 >> 1) & 7)) << 4);
         } else {
-          const int chunk = (w0 + 32 * i) / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          const int chunk = (w0 + STEP * i) / 8 + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
           const int sw = T == 64 ? (((s4 >> 1) & 1) << 2) : (s4 << 2);
           rd[s][i] = lds + s * stage + (uint32_t)((8 * h32 + s4) * PITCH + ((chunk ^ sw) << 4) + 8 * (lane & 1));
         }
@@ -304,7 +304,7 @@ struct Operand {
   // read i (0 .. READS - 1) of the fragments of substep kk of stage s
   __device__ __forceinline__ void read(int s, int kk, int i, v4i (&fr)[F]) const {
     if constexpr (KC) {
-      fr[i] = *reinterpret_cast<const lds_v4i*>((lds8*)(uintptr_t)rd[s][kk] + i * 32 * 128);
+      fr[i] = *reinterpret_cast<const lds_v4i*>((lds8*)(uintptr_t)rd[s][kk] + i * STEP * 128);
     } else {
       const int f = i >> 1, h = i & 1;
       const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)((lds8*)(uintptr_t)rd[s][f] + (16 * kk + 4 * h) * PITCH));
@@ -538,11 +538,11 @@ __device__ __forceinline__ void plain_rows(const Job& j, const BfArgs& ga, lds8*
   }
 }
 
-template <int EPI, int F>
-__device__ __forceinline__ void epilogue(const Job& j, const BfArgs& ga, v16f (&acc)[F][F], lds8* buf, int wm, int wn, int lane) {
-  unrolled<F>([&](auto fm_) __attribute__((always_inline)) {
+template <int EPI, int F, int ACT>
+__device__ __forceinline__ void epilogue(const Job& j, const BfArgs& ga, v16f (&acc)[ACT][F], lds8* buf, int wm, int wn, int lane) {
+  unrolled<ACT>([&](auto fm_) __attribute__((always_inline)) {
     constexpr int fm = decltype(fm_)::value;
-    const int row0 = (wm * F + fm) * 32;
+    const int row0 = (2 * fm + wm) * 32;
     if (row0 >= j.rows) return;
     stage_f32<F>(acc[fm], buf, lane);
     if constexpr (EPI == EPI_GATED_FWD) {
@@ -597,10 +597,10 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   if (MODE == MGS_GEMM_WGRAD && j.k == 0 && ga.accumulate) return;  // an empty group adds nothing
 
-  Operand<T, AKC, S> oa;
-  Operand<T, BKC, S> ob;
+  Operand<T, AKC, S, 64> oa;
+  Operand<T, BKC, S, 32> ob;
   oa.init(j.a, j.ald, j.a_bytes, j.k, 2 * (j.crow0 - (MODE == MGS_GEMM_WGRAD ? (int64_t)j.g * ga.m : 0)), 16 * F * wave,
-          32 * F * wm, lds0, STAGE, wave, lane);
+          32 * wm, lds0, STAGE, wave, lane);
   if constexpr (EPI == EPI_GATED_FWD) {
     // B rows of a column wave: 16 F gate rows, then the same 16 F up rows; waves 2w and 2w + 1 load them
     const int half = wave & 1;
@@ -616,11 +616,6 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
     else oa.load(slot, n - 2 * F);
   };
   v4i fa[2][F], fb[2][F];
-  constexpr int READS = decltype(oa)::READS + decltype(ob)::READS;
-  auto read = [&](int slot, int kk, int buf, int i) {
-    if (i < decltype(ob)::READS) ob.read(slot, kk, i, fb[buf]);
-    else oa.read(slot, kk, i - decltype(ob)::READS, fa[buf]);
-  };
   const int nsteps = __builtin_amdgcn_readfirstlane((int)((j.k + KSTEP - 1) / KSTEP));
   // loads into a stage: LEAD of them in the step that frees it, one behind every second MFMA, the others in the
   // next step
@@ -631,85 +626,97 @@ void gemm_bf16_kernel(BfArgs ga, GemmTable tt) {
 #pragma unroll
     for (int n = 0; n < (s == S - 1 ? LEAD : NL); ++n) load(s, n);
   }
-  // The accumulators are cleared while the loads are under way, each of its own: of equal values the compiler
-  // would keep one and copy it to the others just ahead of their first MFMA, without the wait states.
-  v16f acc[F][F];
+  // The loop over the K steps for the first ACT of the wave's F row fragments.  with(m) says which load (into stage `to`)
+  // goes with a substep's m-th MFMA, -1 none; behind(m) comes after it.
+  auto run = [&](auto act_) __attribute__((always_inline)) {
+    constexpr int ACT = decltype(act_)::value, MFMAS = F * ACT, EVERY = MFMAS / 8;
+    constexpr int READS = decltype(ob)::READS + decltype(oa)::READS / F * ACT;
+    constexpr int PER = (READS + MFMAS - 1) / MFMAS;  // reads behind each MFMA
+    auto read = [&](int slot, int kk, int buf, int i) {
+      if (i < decltype(ob)::READS) ob.read(slot, kk, i, fb[buf]);
+      else oa.read(slot, kk, i - decltype(ob)::READS, fa[buf]);
+    };
+    auto reads = [&](int slot, int kk, int buf, int m) {
 #pragma unroll
-  for (int fm = 0; fm < F; ++fm)
+      for (int i = m * PER; i < (m + 1) * PER; ++i)
+        if (i < READS) read(slot, kk, buf, i);
+    };
+    // The accumulators are cleared while the loads are under way, each of its own: of equal values the compiler
+    // would keep one and copy it to the others just ahead of their first MFMA, without the wait states.
+    v16f acc[ACT][F];
 #pragma unroll
-    for (int fn = 0; fn < F; ++fn) {
-      acc[fm][fn] = v16f{};
-      if constexpr (F == 4) asm volatile("" : "+a"(acc[fm][fn]));
-    }
-  __builtin_amdgcn_sched_barrier(0);
-  mfma_gap();
-  __builtin_amdgcn_sched_barrier(0);
-  wait_loads<(S - 2) * NL + LEAD>();
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < READS; ++i) read(0, 0, 0, i);
-
-  // The MFMAs of one substep from fragment buffer `buf`, `behind(m)` after the m-th; `with(m)` says which load (into stage
-  // `to`) goes with it, -1 none.
-  constexpr int PER = (READS + F * F - 1) / (F * F);  // reads behind each MFMA
-  auto substep = [&](int buf, int to, auto&& with, auto&& behind) {
-#pragma unroll
-    for (int fm = 0; fm < F; ++fm)
+    for (int fm = 0; fm < ACT; ++fm)
 #pragma unroll
       for (int fn = 0; fn < F; ++fn) {
-        const int m = F * fm + fn, n = with(m);
-        if constexpr (F == 4) {
-          if (n < 0) mfma_pinned(acc[fm][fn], fb[buf][fn], fa[buf][fm]);
-          else if (n < 2 * F) mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], ob.desc, ob.vo[n & (2 * F - 1)], ob.dst[to], (n & (2 * F - 1)) * 1024);
-          else mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], oa.desc, oa.vo[n & (2 * F - 1)], oa.dst[to], (n & (2 * F - 1)) * 1024);
-        } else {
-          acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[buf][fn]),
-                                                                __builtin_bit_cast(v8bf, fa[buf][fm]), acc[fm][fn], 0, 0, 0);
-        }
-        behind(m);
-        if constexpr (F == 4) __builtin_amdgcn_sched_barrier(0);
+        acc[fm][fn] = v16f{};
+        if constexpr (F == 4) asm volatile("" : "+a"(acc[fm][fn]));
       }
-  };
-  auto reads = [&](int slot, int kk, int buf, int m) {
-#pragma unroll
-    for (int i = m * PER; i < (m + 1) * PER; ++i)
-      if (i < READS) read(slot, kk, buf, i);
-  };
-  auto none = [](int) { return -1; };
-  auto step = [&](auto slot_) __attribute__((always_inline)) {
-    constexpr int slot = decltype(slot_)::value, prev = slot == 0 ? S - 1 : slot - 1, next = slot == S - 1 ? 0 : slot + 1;
-    substep(0, prev, [&](int m) { return LEAD < NL && !(m & 1) && LEAD + m / 2 < NL ? LEAD + m / 2 : -1; },
-            [&](int m) { reads(slot, 1, 1, m); });
-    substep(1, 0, none, [&](int m) {
-      reads(slot, 2, 0, m);
-      if (m == F * F - 1) begin();
-    });
-    substep(0, 0, none, [&](int m) { reads(slot, 3, 1, m); });
-    // from here on the next stage is loaded and this one read by every wave
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    wait_loads<(S - 2) * NL>();
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_gap();
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads<(S - 2) * NL + LEAD>();
     __syncthreads();
-    substep(1, slot, [&](int m) { return F == 4 && !(m & 1) ? m / 2 : -1; }, [&](int m) {
-      reads(next, 0, 0, m);
-      if (F != 4 && m == 0) {
+    auto substep = [&](int buf, int to, auto&& with, auto&& behind) {
 #pragma unroll
-        for (int n = 0; n < NL; ++n) load(slot, n);
-      }
-    });
+      for (int fm = 0; fm < ACT; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < F; ++fn) {
+          const int m = F * fm + fn, n = with(m);
+          if constexpr (F == 4) {
+            if (n < 0) mfma_pinned(acc[fm][fn], fb[buf][fn], fa[buf][fm]);
+            else if (n < 2 * F) mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], ob.desc, ob.vo[n & (2 * F - 1)], ob.dst[to], (n & (2 * F - 1)) * 1024);
+            else mfma_with_load(acc[fm][fn], fb[buf][fn], fa[buf][fm], oa.desc, oa.vo[n & (2 * F - 1)], oa.dst[to], (n & (2 * F - 1)) * 1024);
+          } else {
+            acc[fm][fn] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[buf][fn]),
+                                                                  __builtin_bit_cast(v8bf, fa[buf][fm]), acc[fm][fn], 0, 0, 0);
+          }
+          behind(m);
+          if constexpr (F == 4) __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto none = [](int) { return -1; };
+    auto paired = [](int m) { return F == 4 && m % (EVERY ? EVERY : 1) == 0 ? m / (EVERY ? EVERY : 1) : -1; };
+    auto step = [&](auto slot_) __attribute__((always_inline)) {
+      constexpr int slot = decltype(slot_)::value, prev = slot == 0 ? S - 1 : slot - 1, next = slot == S - 1 ? 0 : slot + 1;
+      substep(0, prev, [&](int m) { return LEAD < NL && paired(m) >= 0 ? LEAD + paired(m) : -1; },
+              [&](int m) { reads(slot, 1, 1, m); });
+      substep(1, 0, none, [&](int m) {
+        reads(slot, 2, 0, m);
+        if (m == MFMAS - 1) begin();
+      });
+      substep(0, 0, none, [&](int m) { reads(slot, 3, 1, m); });
+      // from here on the next stage is loaded and this one read by every wave
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      wait_loads<(S - 2) * NL>();
+      __syncthreads();
+      substep(1, slot, paired, [&](int m) {
+        reads(next, 0, 0, m);
+        if (F != 4 && m == 0) {
+#pragma unroll
+          for (int n = 0; n < NL; ++n) load(slot, n);
+        }
+      });
+    };
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read(0, 0, 0, i);
+    for (int st = 0; st < nsteps; st += S)
+      unrolled<S>([&](auto slot) __attribute__((always_inline)) {
+        if (st + decltype(slot)::value < nsteps) step(slot);
+      });
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_drain();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0);  // the masked loads of the steps past the end write LDS too
+    __syncthreads();
+    lds8* buf = lds + wave * (S * STAGE / 4);
+    epilogue<EPI, F, ACT>(j, ga, acc, buf, wm, wn, lane);
   };
-  for (int st = 0; st < nsteps; st += S)
-    unrolled<S>([&](auto slot) __attribute__((always_inline)) {
-      if (st + decltype(slot)::value < nsteps) step(slot);
-    });
-  __builtin_amdgcn_sched_barrier(0);
-  mfma_drain();
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0);  // the masked loads of the steps past the end write LDS too
-  __syncthreads();
-  lds8* buf = lds + wave * (S * STAGE / 4);
-  epilogue<EPI, F>(j, ga, acc, buf, wm, wn, lane);
+  // A group's last tile of at most half the rows leaves out the other row fragments (a wave's fragments are 64 rows apart,
+  // so that this halves the work of all four waves): 32 skewed groups, 16384 rows of 7168 x 2048, gated forward 1030 ->
+  // 1008 us, DGRAD 1000 -> 972; with whole tiles only, nothing changes.
+  if (MODE != MGS_GEMM_WGRAD && F > 1 && j.rows <= T / 2) run(std::integral_constant<int, F == 1 ? 1 : F / 2>{});
+  else run(std::integral_constant<int, F>{});
 }
-
 
 // ------------------------------------------------------------------------------------------ few rows
 //
@@ -980,6 +987,12 @@ int64_t most_rows(const GroupTable& gt) {
   return most;
 }
 
+// The largest tiles that the largest group fills by more than half and that give most CUs one: what a larger tile saves
+// in loads from L2 and LDS outweighs idle CUs down to about three quarters of the 256 (us, sides 64, 128 and 256).  Plain
+// FPROP of 4096 x 4096: 8192 rows (512 tiles of 256) 393, 257, 210; 1024 rows (64 tiles of 256, 256 of 128) 53, 43, 72;
+// 512 rows (32 and 128) 28, 40, 72.  WGRAD of 4096 x 4096 over 512 rows (256 and 1024) 38, 27, 22; of 4096 x 2048 over
+// 2048 rows (128 and 512) 55, 38, 44.  Small groups lose little to half-empty tiles: 16 skewed groups, 1024 rows of
+// 7168 x 2048, FPROP 123, 119, 124, DGRAD 255, 197, 207.
 int tile_side(const BfArgs& ga, int epi, const GroupTable& gt) {
   const int64_t side = ga.mode == MGS_GEMM_WGRAD ? ga.m : most_rows(gt);
   if (side > 128 && tile_count(ga, epi, gt, 4) >= 192) return 4;

@@ -130,6 +130,9 @@ def test_products(M, mode, split, n, k, out):
 # sizes that reach the larger tiles: 128 x 128 and 256 x 256 (by the number of tiles they give)
 LARGE = [("fprop", [100, 300, 0, 77], 6400, 40), ("dgrad", [100, 300, 0, 77], 6400, 40), ("wgrad", [40, 0, 9] * 5, 520, 456),
          ("fprop", [1000, 500], 8192 - 8, 200), ("dgrad", [1000, 500], 8192 - 8, 200), ("wgrad", [70, 0, 129] * 4, 1032, 1000)]
+# groups whose last tile has at most half of its rows, of both sizes
+HALVES = [[1000, 300, 20, 0, 500, 1, 384], [130, 50, 0, 192, 1]]
+LARGE += [(mode, splits, n, k) for mode in ("fprop", "dgrad") for splits, n, k in zip(HALVES, (8192 - 8, 6400), (200, 136))]
 
 
 @pytest.mark.parametrize("mode,splits,n,k", LARGE)
@@ -244,7 +247,7 @@ def test_gated_forward(M, kind, split, f, k):
         assert torch.equal(h, M.grouped_gated_fwd(act_of(kind), splits, xg, wg, bg, pg))
 
 
-@pytest.mark.parametrize("splits,f,k", [([100, 300, 0, 77], 3200, 40), ([1000, 500], 4096 - 8, 200)])
+@pytest.mark.parametrize("splits,f,k", [([100, 300, 0, 77], 3200, 40), ([1000, 500], 4096 - 8, 200), (HALVES[0], 4096 - 8, 200), (HALVES[1], 3200, 136)])
 def test_gated_forward_on_larger_tiles(M, splits, f, k):
     import torch
     x, w, b, p = gated_case("swiglu", splits, f, k, seed=7)
@@ -290,7 +293,7 @@ def test_gated_backward(M, kind, split, f, n):
         check_backward(M, kind, SPLITS[split], f, n, seed=n, probs=probs, pre_dtype=dt)
 
 
-@pytest.mark.parametrize("splits,f,n", [([100, 300, 0, 77], 6400, 40), ([1000, 500], 8192 - 8, 200)])
+@pytest.mark.parametrize("splits,f,n", [([100, 300, 0, 77], 6400, 40), ([1000, 500], 8192 - 8, 200), (HALVES[0], 8192 - 8, 200), (HALVES[1], 6400, 136)])
 def test_gated_backward_on_larger_tiles(M, splits, f, n):
     import torch
     for dt in (torch.bfloat16, torch.float32):
