@@ -12,7 +12,7 @@ import torch
 from . import _native as N
 from .expert_mlp import GATED
 from .gated import _BF16, _F32, _OUT, _gated_act, _given, _groups, _maybe
-from .moe import _call, _check, _fail, _on_stream
+from .moe import _call, _check, _fail, _int32, _on_stream
 
 _U8 = (torch.uint8,)
 
@@ -21,7 +21,11 @@ class W4Tensor:
     """Packed 4-bit weights [experts, n, k]: `data` (uint8), `shape`, `group`, `zeros` (whether it has zero points)."""
 
     def __init__(self, data, shape, group, zeros):
-        self.data, self.shape, self.group, self.zeros = data, tuple(int(v) for v in shape), int(group), bool(zeros)
+        self.shape, self.group, self.zeros = tuple(int(v) for v in shape), int(group), bool(zeros)
+        size = _nbytes(*self.shape, self.group, self.zeros)
+        if not isinstance(data, torch.Tensor) or data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() != size:
+            _fail("data must be a contiguous uint8 tensor of %d bytes", size)
+        self.data = data
 
     @property
     def device(self):
@@ -40,6 +44,8 @@ def _check_w4(what, w, device=None):
 
 
 def _nbytes(e, n, k, group, zeros):
+    _int32("experts", e)
+    _int32("group", group)
     size = N.LIB.mgs_w4_nbytes(e, n, k, group, int(zeros))
     if size < 0:
         N._check(int(size))
@@ -72,6 +78,7 @@ def w4_quantize(w, group=128, zeros=True, stream=None):
     takes."""
     if stream is not None:
         return _on_stream(stream, w, w4_quantize, w, group, zeros)
+    _int32("group", group)
     _check("w", w, _BF16, 3)
     e, n, k = w.shape
     _nbytes(e, n, k, group, zeros)  # (refuses what does not fit)
@@ -144,7 +151,8 @@ class W4GatedMLP:
     def forward(self, x1, probs, splits):
         """x1 [M, H] BF16, probs [M] FP32 or None, `splits` host split sizes or an N.DeviceGroups -> [M, H] BF16."""
         if isinstance(splits, N.DeviceGroups):
-            splits.update()
+            with torch.cuda.device(self.w1.device):
+                splits.update()
         h = grouped_gated_w4(self.act, splits, x1, self.w1, self.b1, probs)
         self.ctx = {}  # nothing is kept; MoELayer marks it
         return grouped_gemm_w4(splits, h, self.w2, self.b2)

@@ -123,3 +123,22 @@ def test_python_refusals():
     ]:
         with pytest.raises(ValueError, match=match):
             fn()
+
+
+def test_packed_weights_have_their_size():
+    """A W4Tensor around other data would let the products read past its end; 32-bit arguments are not cut off."""
+    import torch
+    import moe_grouped_scaled_amd as m
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8)
+    size = m._native.LIB.mgs_w4_nbytes(2, 40, 96, 32, 1)
+    t = m.W4Tensor(u8(size), (2, 40, 96), 32, True)
+    assert t.nbytes() == size and t.shape == (2, 40, 96)
+    for data in (u8(size - 1), u8(size + 16), u8(size).view(torch.int8), u8(2 * size)[::2], 3):
+        with pytest.raises(ValueError, match="%d bytes" % size):
+            m.W4Tensor(data, (2, 40, 96), 32, True)
+    with pytest.raises(m.MgsError, match="not 32, 64 or 128"):
+        m.W4Tensor(u8(size), (2, 40, 96), 48, True)
+    for fn in (lambda: m.W4Tensor(u8(size), (2, 40, 96), 2 ** 32 + 32, True), lambda: m.w4_quantize(u8(4), group=2 ** 32 + 32),
+               lambda: m.w4_quantize(u8(4), group=-32), lambda: m.W4Tensor(u8(size), (2 ** 32 + 2, 40, 96), 32, True)):
+        with pytest.raises(ValueError, match="out of range"):
+            fn()
