@@ -193,12 +193,14 @@ class GatedMLP:
     def forward(self, x1, probs, splits):
         """`splits`: host split sizes, or an N.DeviceGroups, whose offsets the step computes first, so that a captured
         graph of it follows the split sizes held in the device tensor."""
-        _check("x1", x1, _BF16, 2, self.w1.device, shape=(x1.shape[0], self.h))
-        if isinstance(splits, N.DeviceGroups):
-            splits.update()
-        else:
-            splits = [int(s) for s in splits]
+        _check("x1", x1, _BF16, 2, self.w1.device)
+        if x1.shape[1] != self.h:
+            _fail("x1 has rows of width %d, w1 of width %d", x1.shape[1], self.h)
         with torch.cuda.device(x1.device):
+            if isinstance(splits, N.DeviceGroups):
+                splits.update()
+            else:
+                splits = [int(s) for s in splits]
             keep_pre = self.grad_below_fc2 or (self.grad_fc2 and self.recompute)
             pre = torch.empty((x1.shape[0], self.f_in), dtype=self.save_dtype, device=x1.device) if keep_pre else None
             a = grouped_gated_fwd(self.act, splits, x1, self.w1, self.b1, probs, pre=pre)
