@@ -8,6 +8,8 @@
 // the two.  No result depends on timing.  The tensors' addresses travel in the kernel arguments, TENSORS of them a
 // launch; where there are more, such launches first put them into the workspace, so that the norm and the scaling
 // are one launch each (400 tensors, 1.2 GB: in four launches each they took 219 and 577 us).
+// Bound by memory: those 400 tensors take 199 us for the norm (6.1 TB/s) and 478 us for the scaling (5.1 TB/s read and
+// written), 3.2 GB of FP32 gradients into BF16 518 and 905 us; 12 tensors of 300000 elements 3.8 and 4.3 us.
 #include <algorithm>
 #include <cmath>
 #include <new>
