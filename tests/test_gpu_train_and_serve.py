@@ -118,3 +118,75 @@ def test_trained_clipped_quantized_and_served(M, captured):
         # and no further from the trained layer than 4 bits take it: a step of 1/15 of a group's range, about 4 deviations
         # of its weights, leaves 4 / 15 / sqrt(12) = 0.077 of a weight's size, twice in a block of three products of them
         assert rel(y, layer.forward(x[:tokens], logits[:tokens]).double().cpu()) < 0.25
+
+
+def test_two_streams_at_once(M):
+    """Two blocks that train and a third that serves, each on a stream of its own at the same time: as one after the other."""
+    import torch
+    gen = torch.Generator().manual_seed(7)
+    splits, h, f = [200, 0, 313], 256, 512
+    m = sum(splits)
+    w1, w2 = normal(gen, 3, 2 * f, h, std=h ** -0.5).cuda(), normal(gen, 3, h, f, std=f ** -0.5).cuda()
+    q1, q2 = (M.w4_pack(*M.w4_quantize(w)) for w in (w1, w2))
+    xs, dys = ([normal(gen, m, h).cuda() for _ in range(2)] for _ in range(2))
+    p = torch.rand(m, generator=gen).cuda()
+
+    def trained(i):
+        mlp = M.GatedMLP("swiglu", w1, w2)
+        out = []
+        for _ in range(4):
+            y = mlp.forward(xs[i], p, splits)
+            g = mlp.backward(dys[i])
+            out = [y, g["dx1"], g["dprobs"], M.clip_grad_norm([g["dw1"], g["dw2"]], 0.5), g["dw1"], g["dw2"]]
+        return out
+
+    def served(_):
+        mlp = M.W4GatedMLP("swiglu", q1, q2)
+        return [mlp.forward(xs[0], p, splits) for _ in range(8)]
+
+    work = [(trained, 0), (trained, 1), (served, 0)]
+    ref = [fn(i) for fn, i in work]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in work], []
+    for (fn, i), s in zip(work, streams):
+        with torch.cuda.stream(s):
+            got.append(fn(i))
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_two_graphs_share_a_workspace(M):
+    """Two captured clips of different gradients with one workspace, replayed in turn: each its own norm, every time."""
+    import torch
+    gen = torch.Generator().manual_seed(8)
+    sizes = [[300000, 7], [5] * 150 + [2000000]]
+    grads = [[torch.empty(n, device="cuda") for n in s] for s in sizes]
+    outs = [[torch.empty_like(g) for g in gs] for gs in grads]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    run = lambda i: M.clip_grad_norm(grads[i], 1.0, out=outs[i], workspace=ws)
+    for i in range(2):
+        for g in grads[i]:
+            g.normal_()
+        run(i)
+    torch.cuda.synchronize()
+    graphs, norms = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            norms.append(run(i))
+    for r in range(3):
+        for i in range(2):
+            for g in grads[i]:
+                g.copy_(torch.randn(g.numel(), generator=gen) * (r + 1))
+        for i in (0, 1, 0):
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            exact = norm64([g.cpu() for g in grads[i]])
+            assert abs(norms[i].item() - exact) <= 1.01 * 2.0 ** -24 * exact
+            for g, o in zip(grads[i], outs[i]):
+                want = g.double() / (exact + 1e-6)
+                assert ((o.double() - want).abs() <= 3 * 2.0 ** -24 * want.abs() + 1e-44).all()
+        assert torch.equal(run(0), norms[0])
