@@ -38,19 +38,20 @@ def _run(grads, clip, max_norm, eps, out, workspace, norm):
     # mgs_grad rows: address, output's address, elements, the two types in one word
     rows, index, types, is_tensor = [], dev.index, _TYPES, torch.Tensor
     for i, g in enumerate(grads):
-        if not isinstance(g, is_tensor) or g.dtype not in types or g.get_device() != index or not g.is_contiguous():
+        o = g if out is None else out[i]
+        t, u = (types.get(g.dtype), types.get(o.dtype)) if isinstance(g, is_tensor) and isinstance(o, is_tensor) else (None, None)
+        if (t is None or u is None or g.get_device() != index or o.get_device() != index
+                or not (g.is_contiguous() and o.is_contiguous())):
             _tensor("grads[%d]" % i, g, dev)
-        t, n = types[g.dtype], g.numel()
-        if out is None:
+            _tensor("out[%d]" % i, o, dev)
+        n = g.numel()
+        if o is g:
             at = g.data_ptr()
             rows += (at, at, n, t << 32 | t)
             continue
-        o = out[i]
-        if not isinstance(o, is_tensor) or o.dtype not in types or o.get_device() != index or not o.is_contiguous():
-            _tensor("out[%d]" % i, o, dev)
         if o.numel() != n:
             _fail("out[%d] has %d elements, expected %d", i, o.numel(), n)
-        rows += (g.data_ptr(), o.data_ptr(), n, types[o.dtype] << 32 | t)
+        rows += (g.data_ptr(), o.data_ptr(), n, u << 32 | t)
     table = array.array("q", rows)
     at = table.buffer_info()[0]
     need = N.LIB.mgs_grad_norm_workspace_bytes(len(grads), at)
