@@ -442,7 +442,8 @@ int mgs_grouped_gemm_bf16(int32_t mode, const mgs_groups* groups, int64_t m, int
                           void* stream);
 
 /* Forward of the gated block in one kernel: with [gate | up] = x_g W_g^T + bias in FP32,
- *   h = act(gate, up) * probs[row], rounded to BF16 once.
+ *   h = act(gate, up) * probs[row], rounded to BF16 once.  The clamps keep a NaN: h is NaN where
+ *   gate or up is, and so are, in the backward, the row's dprobs and what the derivatives make of it in dpre.
  *   act      a gated kind (SWIGLU, CLAMPED_SWIGLU, GLU)
  *   x_bf16   [M x k]; w_bf16 [E x 2f x k]; bias_bf16 [E x 2f] nullable; probs [M] FP32, NULL means 1
  *   h_bf16   [M x f]

@@ -200,9 +200,9 @@ __device__ __forceinline__ void st_bf16x8(uint16_t* p, const float (&v)[8]) {
   st16<NT>(p, v4u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])});
 }
 __device__ __forceinline__ float act_gated_of(int kind, float g, float u, const ActArgs& aa) {
-  return kind == MGS_ACT_SWIGLU ? act_gated<MGS_ACT_SWIGLU>(g, u, aa)
-         : kind == MGS_ACT_GLU  ? act_gated<MGS_ACT_GLU>(g, u, aa)
-                                : act_gated<MGS_ACT_CLAMPED_SWIGLU>(g, u, aa);
+  return kind == MGS_ACT_SWIGLU ? act_gated<MGS_ACT_SWIGLU, true>(g, u, aa)
+         : kind == MGS_ACT_GLU  ? act_gated<MGS_ACT_GLU, true>(g, u, aa)
+                                : act_gated<MGS_ACT_CLAMPED_SWIGLU, true>(g, u, aa);
 }
 
 // What the backward reads of a gate or an up value: its BF16 rounding, but on the same side of the clamp.  The
@@ -400,7 +400,7 @@ __device__ __forceinline__ void gated_fwd_rows(const Job& j, const BfArgs& ga, l
     add_bf16x8(v, bg);
     add_bf16x8(u, bu);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) h[t] = act_gated<KIND>(v[t], u[t], ga.act) * s;
+    for (int t = 0; t < 8; ++t) h[t] = act_gated<KIND, true>(v[t], u[t], ga.act) * s;
     st_bf16x8<NT>(static_cast<uint16_t*>(ga.c) + gr * ga.n + gc, h);
     if (ga.pre_out && !ga.pre_f32) {
       if constexpr (KIND == MGS_ACT_CLAMPED_SWIGLU) {
@@ -481,7 +481,7 @@ __device__ __forceinline__ void gated_bwd_rows(const Job& j, const BfArgs& ga, l
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
       float a, bg, bu;
-      dact_gated<KIND>(g[t], u[t], ga.act, a, bg, bu);
+      dact_gated<KIND, true>(g[t], u[t], ga.act, a, bg, bu);
       dp += v[t] * a;
       const float d = v[t] * now.s;
       dg[t] = d * bg;

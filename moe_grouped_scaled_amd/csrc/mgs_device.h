@@ -310,22 +310,36 @@ __device__ __forceinline__ float dact_unary(float x, const ActArgs& aa) {
   }
 }
 
+// The clamps of the clamped SwiGLU: min(v, hi), and v between -hi and hi.  fminf and fmaxf drop a NaN (of the gate it
+// became the limit, of up minus the limit), which is what the quantized activations do, whose formats take finite
+// values; KEEP_NAN keeps it (V_MINIMUM3 / V_MAXIMUM3, one instruction a bound like the others).
+template <bool KEEP_NAN>
+__device__ __forceinline__ float clamp_above(float v, float hi) {
+  if constexpr (KEEP_NAN) return __builtin_elementwise_minimum(v, hi);
+  else return fminf(v, hi);
+}
+template <bool KEEP_NAN>
+__device__ __forceinline__ float clamp_both(float v, float hi) {
+  if constexpr (KEEP_NAN) return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -hi), hi);
+  else return fminf(fmaxf(v, -hi), hi);
+}
+
 // a(gate, up) for gated kinds
-template <int KIND>
+template <int KIND, bool KEEP_NAN = false>
 __device__ __forceinline__ float act_gated(float g, float u, const ActArgs& aa) {
   if constexpr (KIND == MGS_ACT_SWIGLU) {
     return g * sigmoidf_(g) * u;
   } else if constexpr (KIND == MGS_ACT_GLU) {
     return sigmoidf_(g) * u;
   } else {
-    float gc = fminf(g, aa.limit);
-    float uc = fminf(fmaxf(u, -aa.limit), aa.limit);
+    float gc = clamp_above<KEEP_NAN>(g, aa.limit);
+    float uc = clamp_both<KEEP_NAN>(u, aa.limit);
     return gc * sigmoidf_(aa.alpha * gc) * (uc + aa.beta);
   }
 }
 
 // (a, da/dgate, da/dup) for gated kinds
-template <int KIND>
+template <int KIND, bool KEEP_NAN = false>
 __device__ __forceinline__ void dact_gated(float g, float u, const ActArgs& aa, float& a, float& dg,
                                            float& du) {
   if constexpr (KIND == MGS_ACT_SWIGLU) {
@@ -340,14 +354,20 @@ __device__ __forceinline__ void dact_gated(float g, float u, const ActArgs& aa, 
     dg = u * (sg * (1.0f - sg));
     du = sg;
   } else {
-    float gc = fminf(g, aa.limit);
-    float uc = fminf(fmaxf(u, -aa.limit), aa.limit);
+    float gc = clamp_above<KEEP_NAN>(g, aa.limit);
+    float uc = clamp_both<KEEP_NAN>(u, aa.limit);
     float sg = sigmoidf_(aa.alpha * gc);
     float silu = gc * sg;
     float up = uc + aa.beta;
     a = silu * up;
-    dg = g <= aa.limit ? up * sg * (1.0f + aa.alpha * gc * (1.0f - sg)) : 0.0f;
-    du = (u >= -aa.limit && u <= aa.limit) ? silu : 0.0f;
+    if constexpr (KEEP_NAN) {
+      // a NaN of either half reaches both derivatives, the masked ones too: v - v is 0, or NaN of a NaN
+      dg = g > aa.limit ? up - up : up * sg * (1.0f + aa.alpha * gc * (1.0f - sg));
+      du = fabsf(u) > aa.limit ? silu - silu : u != u ? u : silu;
+    } else {
+      dg = g <= aa.limit ? up * sg * (1.0f + aa.alpha * gc * (1.0f - sg)) : 0.0f;
+      du = (u >= -aa.limit && u <= aa.limit) ? silu : 0.0f;
+    }
   }
 }
 

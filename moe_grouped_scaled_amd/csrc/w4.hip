@@ -228,9 +228,9 @@ __global__ __launch_bounds__(64 * WAVES) void w4_kernel(W4Args a, GroupTable gt,
           u += bf16lo(a.bias[g * 2 * a.n + a.n + gc]);
         }
         const float s = a.probs ? a.probs[gr] : 1.0f;
-        v = (a.act.kind == MGS_ACT_SWIGLU ? act_gated<MGS_ACT_SWIGLU>(v, u, a.act)
-             : a.act.kind == MGS_ACT_GLU  ? act_gated<MGS_ACT_GLU>(v, u, a.act)
-                                          : act_gated<MGS_ACT_CLAMPED_SWIGLU>(v, u, a.act)) * s;
+        v = (a.act.kind == MGS_ACT_SWIGLU ? act_gated<MGS_ACT_SWIGLU, true>(v, u, a.act)
+             : a.act.kind == MGS_ACT_GLU  ? act_gated<MGS_ACT_GLU, true>(v, u, a.act)
+                                          : act_gated<MGS_ACT_CLAMPED_SWIGLU, true>(v, u, a.act)) * s;
       } else if (a.bias) {
         v += bf16lo(a.bias[g * a.n + gc]);
       }
