@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "launch_size.h"
 #include "lds_dma.h"
 #include "mgs_device.h"
 #include "mgs_span.h"
@@ -400,10 +401,10 @@ int w4_launch(const W4Args& a, bool gated, int group, bool zeros, const GroupTab
   if (gt.dev) passes = gt.total_rows > xr ? 2 : 1;
   else
     for (int g = 0; g < gt.num_groups; ++g) passes = std::max<int64_t>(passes, (gt.row_off[g + 1] - gt.row_off[g] + xr - 1) / xr);
-  passes = std::min<int64_t>(passes, 16);
-  const int64_t grid = (a.n + tn - 1) / tn * gt.num_groups * passes;
-  if (grid > INT32_MAX / 1024) return fail(MGS_ERR_SHAPE, "too many tiles");
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * waves), 0, st, a, gt, (int)passes);
+  // (256 experts x 2^20 weight rows, the most that check_w4 takes, are 2^23 workgroups of 256 threads)
+  const int64_t base = (a.n + tn - 1) / tn * gt.num_groups;
+  passes = shared_passes(passes, base, 64 * waves);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(base * passes)), dim3(64 * waves), 0, st, a, gt, (int)passes);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(MGS_ERR_HIP, "HIP launch error: %s", hipGetErrorString(e));
   return ok();
