@@ -22,6 +22,7 @@
 #include <cstring>
 #include <type_traits>
 
+#include "launch_size.h"
 #include "lds_dma.h"
 #include "mgs_device.h"
 #include "mgs_span.h"
@@ -1049,7 +1050,8 @@ int launch(const BfArgs& ga, int epi, const GroupTable& gt, GemmTable* dev_table
       else kern = rows_bf16_kernel<EPI_PLAIN, 32, 4, 4, 1>, tn = 64;
     }
     const int64_t grid = (int64_t)gt.num_groups * ((ga.n + tn - 1) / tn);
-    if (grid > INT32_MAX / 1024) return fail(MGS_ERR_SHAPE, "too many tiles");
+    // (beyond: only the gated form of 256 experts x 2^20 pairs)
+    if (grid > most_workgroups(64 * waves)) return fail(MGS_ERR_SHAPE, "too many tiles");
     hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * waves), 0, st, ga, gt);
   } else {
     const int f = tile_side(ga, epi, gt), tm = 64 * f;

@@ -3,7 +3,7 @@
 import pytest
 
 import test_gpu_w4 as W
-from test_gpu_gated import UACT, UBF, act64, act_of, check, cuda
+from test_gpu_gated import U32, UACT, UBF, act64, act_of, check, gated64
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,33 @@ def test_w4_passes_of_many_experts(M, experts, f, rows):
     a, dg, du, mag_a, mag_g = act64("swiglu", pre[:, :f], pre[:, f:])
     tol = 2 * (dg.abs() + mag_g) * d[:, :f] + (pre[:, :f].abs() + 1) * d[:, f:] + UACT * mag_a
     check(h[some], a, tol + UBF * a.abs(), "h")
+
+
+@pytest.mark.parametrize("n,rows", [((1 << 18) - 8, 1), (1 << 18, 20)])
+def test_few_bf16_rows_of_many_experts(M, n, rows):
+    """2^21 workgroups of 32 weight rows for up to 16 rows, 2^20 of 64 for more."""
+    import torch
+    experts, k, g = 256, 8, 253
+    gen = torch.Generator(device="cuda").manual_seed(52)
+    w = torch.randn((experts, n, k), generator=gen, device="cuda", dtype=torch.bfloat16)
+    x = W.rows(rows, k, 53)
+    splits = [0] * experts
+    splits[g] = rows
+    got = M.grouped_gemm_bf16("fprop", splits, x.cuda(), w, out_dtype=torch.float32)
+    wg = w[g].cpu().double()
+    ref, mag = x.double() @ wg.t(), x.double().abs() @ wg.t().abs()
+    check(got, ref, (k + 2) * U32 * mag + U32 * ref.abs(), "c")
+
+
+@pytest.mark.parametrize("f", [1 << 17])
+def test_few_gated_rows_of_many_experts(M, f):
+    import torch
+    experts, k, g, rows = 256, 8, 250, 3
+    gen = torch.Generator(device="cuda").manual_seed(54)
+    w = torch.randn((experts, 2 * f, k), generator=gen, device="cuda", dtype=torch.bfloat16) * k ** -0.5
+    x = W.rows(rows, k, 55)
+    splits = [0] * experts
+    splits[g] = rows
+    h = M.grouped_gated_fwd(act_of("glu"), splits, x.cuda(), w)
+    ref, tol, _, _ = gated64("glu", [rows], x, w[g:g + 1].cpu(), None, None)
+    check(h, ref, tol + UBF * ref.abs(), "h")

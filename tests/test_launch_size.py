@@ -1,4 +1,5 @@
-"""How many workgroups share the passes of a 4-bit product over a group's rows (host arithmetic, built by itself)."""
+"""How many workgroups a launch takes, and how many share the passes of a 4-bit product over a group's rows (host arithmetic,
+built by itself)."""
 
 import os
 import subprocess
@@ -12,6 +13,7 @@ DRIVER = r"""
 #include <cstdlib>
 #include "launch_size.h"
 int main(int argc, char** argv) {
+  if (argc == 2) std::printf("%lld\n", (long long)mgs::most_workgroups(std::atoi(argv[1])));
   for (int i = 1; i + 2 < argc; i += 3)
     std::printf("%lld\n", (long long)mgs::shared_passes(std::atoll(argv[i]), std::atoll(argv[i + 1]), std::atoi(argv[i + 2])));
 }
@@ -39,7 +41,14 @@ def shared(tmp_path_factory):
         out = subprocess.run([exe] + [str(v) for c in cases for v in c[:3]], check=True, stdout=subprocess.PIPE, text=True, timeout=60)
         return [int(v) for v in out.stdout.split()]
 
+    run.exe = exe
     return run
+
+
+@pytest.mark.parametrize("threads", [64, 128, 256, 512])
+def test_most_workgroups(shared, threads):
+    most = int(subprocess.run([shared.exe, str(threads)], check=True, stdout=subprocess.PIPE, text=True, timeout=60).stdout)
+    assert most * threads < 1 << 32 <= (most + 1) * threads
 
 
 def test_shared_passes(shared):
