@@ -161,7 +161,10 @@ class GatedMLP:
     gradients are then those at the rounded values, and carry that rounding's error beside their own), and with `recompute`
     regenerates the second linear's input from it in the backward instead of keeping that too (from BF16, the regenerated
     rows differ from the forward's by the rounding of [gate | up]).  Rows are one captured step's own:
-    every forward allocates its outputs."""
+    every forward allocates its outputs.
+
+    With `delay_wgrad` the weight and bias gradients of a backward are computed by backward_dw(), before the next
+    backward (which is refused while they are pending)."""
 
     def __init__(self, kind, w1, w2, b1=None, b2=None, recompute=False, delay_wgrad=False, limit=7.0, alpha=1.0, beta=0.0,
                  grad_x1=True, grad_probs=True, grad_fc1=True, grad_fc2=True, dw_dtype=torch.float32,
@@ -213,6 +216,9 @@ class GatedMLP:
         c = self.ctx
         if c is None:
             _fail("backward() without a forward")
+        if self.pending_wgrad is not None and (self.grad_fc1 or self.grad_fc2):
+            _fail("the weight gradients of the last backward() are still to be computed: backward_dw() (or drop them: "
+                  "pending_wgrad = None)")
         splits, pre, a = c["splits"], c["pre"], c["a"]
         m = sum(splits) if isinstance(splits, list) else splits.max_rows
         _check("dy2", dy2, _BF16, 2, self.w1.device, shape=(m, self.h))
@@ -234,7 +240,10 @@ class GatedMLP:
                                   x1=c["x1"])
         self.ctx = None
         if not self.delay_wgrad:
-            grads.update(self.backward_dw())
+            try:
+                grads.update(self.backward_dw())
+            finally:
+                self.pending_wgrad = None
         return grads
 
     def backward_dw(self, dw1=None, dw2=None, accumulate=False):

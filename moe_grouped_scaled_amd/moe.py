@@ -324,14 +324,14 @@ class MoELayer:
         if (self.mlp.ctx or {}).get("owner") is not c["mark"]:
             self.ctx = None
             _fail("the expert MLP has run another forward or its backward since: what this one saved is gone")
-        self.ctx = None
         with torch.cuda.device(dy.device):
             drows = torch.empty((c["cap"], self.mlp.h), dtype=torch.bfloat16, device=dy.device)
             if "w" in c:  # the combine's weights
                 dw = moe_combine_bwd(row, dy, drows, rows=c["y_rows"], weights=c["w"])
             else:
                 dw = moe_combine_bwd(row, dy, drows)
-            grads = self.mlp.backward(drows)
+            grads = self.mlp.backward(drows)  # (may refuse: then this forward can still be gone back from)
+            self.ctx = None
             dx_rows, dprobs = grads.pop("dx1", None), grads.pop("dprobs", None)
             if "w" in c:
                 dprobs = None  # of the rows' scales of 1
