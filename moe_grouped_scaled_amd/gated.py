@@ -150,6 +150,21 @@ def grouped_gated_bwd(act, split_sizes, dy, w2, pre, probs=None, dpre=None, h=No
     return dpre
 
 
+def _marks(*tensors):
+    """Of each tensor that is kept by reference, torch's count of its in-place changes.  None, which nothing is compared
+    with: for a part of a larger storage (whose other parts may change), for a tensor without a count, and inside a
+    captured graph, whose buffers change between replays."""
+    if torch.cuda.is_current_stream_capturing():
+        return (None,) * len(tensors)
+    return tuple(None if t is None or t.is_inference() or t.untyped_storage().nbytes() != t.numel() * t.element_size()
+                 else t._version for t in tensors)
+
+
+def _unchanged(what, t, mark, since):
+    if mark is not None and t._version != mark:
+        _fail("%s was changed in place since the %s: it is kept, not copied, for the gradients", what, since)
+
+
 class GatedMLP:
     """The gated block of every expert in BF16, forward and backward, with the interface of `ExpertMLP`.
 
@@ -164,7 +179,10 @@ class GatedMLP:
     every forward allocates its outputs.
 
     With `delay_wgrad` the weight and bias gradients of a backward are computed by backward_dw(), before the next
-    backward (which is refused while they are pending)."""
+    backward (which is refused while they are pending).  x1, probs and dy2 are kept, not copied (an `ExpertMLP` keeps
+    quantized copies): they, and the split sizes of a DeviceGroups, stay as they are until the gradients that need them are
+    computed, x1 and dy2 until backward_dw().  An in-place change by torch of a tensor that fills its storage is refused;
+    a change of a part of a larger buffer, by a kernel that is given the address, or by a graph's replay is not seen."""
 
     def __init__(self, kind, w1, w2, b1=None, b2=None, recompute=False, delay_wgrad=False, limit=7.0, alpha=1.0, beta=0.0,
                  grad_x1=True, grad_probs=True, grad_fc1=True, grad_fc2=True, dw_dtype=torch.float32,
@@ -208,8 +226,10 @@ class GatedMLP:
             pre = torch.empty((x1.shape[0], self.f_in), dtype=self.save_dtype, device=x1.device) if keep_pre else None
             a = grouped_gated_fwd(self.act, splits, x1, self.w1, self.b1, probs, pre=pre)
             y2 = grouped_gemm_bf16("fprop", splits, a, self.w2, bias=self.b2)
-        self.ctx = dict(splits=splits, probs=probs, pre=pre, x1=x1 if self.grad_fc1 else None,
-                        a=a if self.grad_fc2 and not self.recompute else None)
+            x1 = x1 if self.grad_fc1 else None
+            marks = _marks(x1, probs) if keep_pre else (None, None)
+        self.ctx = dict(splits=splits, probs=probs, pre=pre, x1=x1, a=a if self.grad_fc2 and not self.recompute else None,
+                        marks=marks)
         return y2
 
     def backward(self, dy2):
@@ -220,6 +240,9 @@ class GatedMLP:
             _fail("the weight gradients of the last backward() are still to be computed: backward_dw() (or drop them: "
                   "pending_wgrad = None)")
         splits, pre, a = c["splits"], c["pre"], c["a"]
+        x1_mark, probs_mark = c["marks"]
+        _unchanged("x1", c["x1"], x1_mark, "forward")
+        _unchanged("probs", c["probs"], probs_mark, "forward")
         m = sum(splits) if isinstance(splits, list) else splits.max_rows
         _check("dy2", dy2, _BF16, 2, self.w1.device, shape=(m, self.h))
         grads = {}
@@ -236,8 +259,10 @@ class GatedMLP:
                                          dprobs=dprobs)
             if self.grad_x1:
                 grads["dx1"] = grouped_gemm_bf16("dgrad", splits, dpre, self.w1)
-        self.pending_wgrad = dict(splits=splits, dy2=dy2 if self.grad_fc2 else None, a=a, dpre=dpre if self.grad_fc1 else None,
-                                  x1=c["x1"])
+            dy2 = dy2 if self.grad_fc2 else None
+            dy2_mark = _marks(dy2)[0] if self.delay_wgrad else None
+        self.pending_wgrad = dict(splits=splits, dy2=dy2, a=a, dpre=dpre if self.grad_fc1 else None, x1=c["x1"], x1_mark=x1_mark,
+                                  dy2_mark=dy2_mark)
         self.ctx = None
         if not self.delay_wgrad:
             try:
@@ -252,6 +277,8 @@ class GatedMLP:
         if p is None:
             _fail("backward_dw() without a pending backward")
         splits, out = p["splits"], {}
+        _unchanged("x1", p["x1"], p["x1_mark"], "forward")
+        _unchanged("dy2", p["dy2"], p["dy2_mark"], "backward")
         with torch.cuda.device(self.w1.device):
             if self.grad_fc2:
                 out["dw2"] = grouped_gemm_bf16("wgrad", splits, p["dy2"], p["a"], dw2, accumulate=accumulate, out_dtype=self.dw_dtype)

@@ -124,3 +124,89 @@ def test_captured_in_two_graphs(M):
         torch.cuda.synchronize()
         got = {k: v.clone() for k, v in out.items()}
         equal(got, steps(M.GatedMLP("swiglu", *dev), batch, False))
+
+
+@pytest.mark.parametrize("delay", [False, True])
+@pytest.mark.parametrize("name", ["x1", "probs"])
+def test_a_change_after_the_forward_is_refused(M, name, delay):
+    dev, (one, _) = case(70)
+    x, dy, p = one
+    mlp = M.GatedMLP("swiglu", *dev, delay_wgrad=delay)
+    mlp.forward(x, p, SPLITS)
+    (x if name == "x1" else p).mul_(2)
+    with pytest.raises(ValueError, match="%s was changed in place since the forward" % name):
+        mlp.backward(dy)
+    # a new forward takes it as it is now
+    equal(steps(mlp, one, delay), steps(M.GatedMLP("swiglu", *dev), one, False))
+
+
+@pytest.mark.parametrize("name,since", [("x1", "forward"), ("dy2", "backward")])
+def test_a_change_before_delayed_gradients_is_refused(M, name, since):
+    dev, (one, two) = case(72)
+    x, dy, p = one
+    mlp = M.GatedMLP("swiglu", *dev, delay_wgrad=True)
+    mlp.forward(x, p, SPLITS)
+    mlp.backward(dy)
+    p.zero_()  # (nothing needs it any more)
+    (x if name == "x1" else dy).copy_(two[0])
+    for _ in range(2):
+        with pytest.raises(ValueError, match="%s was changed in place since the %s" % (name, since)):
+            mlp.backward_dw()
+
+
+def test_what_no_gradient_needs_may_change(M):
+    """x1 without FC1's gradients, dy2 without FC2's, both after a backward that was not delayed, parts of a buffer whose
+    other parts change, and everything after a forward in inference mode."""
+    import torch
+    dev, (one, two) = case(74)
+    x, dy, p = [t.clone() for t in one]
+    want = steps(M.GatedMLP("swiglu", *dev), one, False)
+    for off, var in (("grad_fc1", x), ("grad_fc2", dy)):
+        mlp = M.GatedMLP("swiglu", *dev, delay_wgrad=True, **{off: False})
+        mlp.forward(x, p, SPLITS)
+        if off == "grad_fc1":
+            x.zero_()
+        g = mlp.backward(dy)
+        if off == "grad_fc2":
+            dy.zero_()
+        g.update(mlp.backward_dw())
+        for k in g:
+            assert torch.equal(g[k], want[k]), k
+        x, dy, p = [t.clone() for t in one]
+    slots = torch.zeros((2, 65, H), dtype=torch.bfloat16, device="cuda")
+    slots[0] = x
+    mlp = M.GatedMLP("swiglu", *dev, delay_wgrad=True)
+    got = dict(y=mlp.forward(slots[0], p, SPLITS))
+    slots[1] = two[0]
+    got.update(mlp.backward(dy))
+    slots[1] = 0
+    got.update(mlp.backward_dw())
+    equal(got, want)
+    with torch.inference_mode():
+        xi = x.clone()
+        assert torch.equal(mlp.forward(xi, p, SPLITS), want["y"])
+        xi.zero_()
+
+
+def test_graphs_whose_inputs_change_between_their_captures(M):
+    import torch
+    dev, (one, two) = case(76)
+    x, dy, p = [t.clone() for t in one]
+    mlp = M.GatedMLP("swiglu", *dev, delay_wgrad=True)
+    steps(mlp, (x, dy, p), True)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(a):
+        out = dict(y=mlp.forward(x, p, SPLITS))
+        out.update(mlp.backward(dy))
+    for t, s in zip((x, dy, p), two):
+        t.copy_(s)
+    with torch.cuda.graph(b):
+        out.update(mlp.backward_dw())
+    for batch in (two, one, two):
+        for t, s in zip((x, dy, p), batch):
+            t.copy_(s)
+        a.replay()
+        b.replay()
+        torch.cuda.synchronize()
+        equal({k: v.clone() for k, v in out.items()}, steps(M.GatedMLP("swiglu", *dev), batch, False))
