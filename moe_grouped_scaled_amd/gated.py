@@ -279,16 +279,31 @@ class GatedMLP:
         splits, out = p["splits"], {}
         _unchanged("x1", p["x1"], p["x1_mark"], "forward")
         _unchanged("dy2", p["dy2"], p["dy2_mark"], "backward")
+        # (all is checked and allocated before the first launch: a call that fails has added nothing)
+        if self.grad_fc2:
+            out["dw2"] = self._weight_grad("dw2", dw2, (self.e, self.h, self.f), accumulate)
+        if self.grad_fc1:
+            out["dw1"] = self._weight_grad("dw1", dw1, (self.e, self.f_in, self.h), accumulate)
+        for name, bias in (("db2", self.b2 if self.grad_fc2 else None), ("db1", self.b1 if self.grad_fc1 else None)):
+            if bias is not None:
+                out[name] = torch.empty(bias.shape, dtype=torch.float32, device=bias.device)
         with torch.cuda.device(self.w1.device):
             if self.grad_fc2:
-                out["dw2"] = grouped_gemm_bf16("wgrad", splits, p["dy2"], p["a"], dw2, accumulate=accumulate, out_dtype=self.dw_dtype)
-                if self.b2 is not None:
-                    out["db2"] = torch.empty((self.e, self.h), dtype=torch.float32, device=self.w1.device)
-                    N.grouped_col_sum(splits, self.h, p["dy2"], out["db2"])
+                grouped_gemm_bf16("wgrad", splits, p["dy2"], p["a"], out["dw2"], accumulate=accumulate)
+            if "db2" in out:
+                N.grouped_col_sum(splits, self.h, p["dy2"], out["db2"])
             if self.grad_fc1:
-                out["dw1"] = grouped_gemm_bf16("wgrad", splits, p["dpre"], p["x1"], dw1, accumulate=accumulate, out_dtype=self.dw_dtype)
-                if self.b1 is not None:
-                    out["db1"] = torch.empty((self.e, self.f_in), dtype=torch.float32, device=self.w1.device)
-                    N.grouped_col_sum(splits, self.f_in, p["dpre"], out["db1"])
+                grouped_gemm_bf16("wgrad", splits, p["dpre"], p["x1"], out["dw1"], accumulate=accumulate)
+            if "db1" in out:
+                N.grouped_col_sum(splits, self.f_in, p["dpre"], out["db1"])
         self.pending_wgrad = None
         return out
+
+    def _weight_grad(self, name, t, shape, accumulate):
+        """The weight gradient `name` to write or, with `accumulate`, to add into: `t`, or a new one."""
+        if accumulate and t is None:
+            _fail("accumulate needs a %s to add into", name)
+        t = _given(name, t, (self.dw_dtype,) if t is None else _F32 if accumulate else _OUT, shape, self.w1.device)
+        if t.data_ptr() % 16:
+            _fail("%s must be 16-byte aligned", name)
+        return t
