@@ -18,8 +18,8 @@ _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _OUT = (torch.bfloat16, torch.float32)
 
 
-def _groups(split_sizes, rows, experts, device):
-    """The library's view of the groups, which must cover `rows` rows of `experts` experts."""
+def _check_groups(split_sizes, rows, experts, device):
+    """The groups must cover `rows` rows of `experts` experts on `device`."""
     n = len(split_sizes)
     if n != experts:
         _fail("split_sizes has %d entries, the weights %d experts", n, experts)
@@ -31,6 +31,11 @@ def _groups(split_sizes, rows, experts, device):
             _fail("the split sizes are on %s, the tensors on %s", split_sizes.table.device, device)
     elif sum(split_sizes) != rows:
         _fail("the split sizes add up to %d, the tensors have %d rows", sum(split_sizes), rows)
+
+
+def _groups(split_sizes, rows, experts, device):
+    """The library's view of the groups (see _check_groups)."""
+    _check_groups(split_sizes, rows, experts, device)
     return N._GroupsArg(split_sizes)
 
 
@@ -217,6 +222,9 @@ class GatedMLP:
         _check("x1", x1, _BF16, 2, self.w1.device)
         if x1.shape[1] != self.h:
             _fail("x1 has rows of width %d, w1 of width %d", x1.shape[1], self.h)
+        if isinstance(splits, N.DeviceGroups):
+            # (ahead of the update, whose kernel would write a table on another device from this one)
+            _check_groups(splits, x1.shape[0], self.e, x1.device)
         with torch.cuda.device(x1.device):
             if isinstance(splits, N.DeviceGroups):
                 splits.update()

@@ -11,7 +11,7 @@ import torch
 
 from . import _native as N
 from .expert_mlp import GATED
-from .gated import _BF16, _F32, _OUT, _gated_act, _given, _groups, _maybe
+from .gated import _BF16, _F32, _OUT, _check_groups, _gated_act, _given, _groups, _maybe
 from .moe import _call, _check, _fail, _int32, _on_stream
 
 _U8 = (torch.uint8,)
@@ -151,7 +151,10 @@ class W4GatedMLP:
     def forward(self, x1, probs, splits):
         """x1 [M, H] BF16, probs [M] FP32 or None, `splits` host split sizes or an N.DeviceGroups -> [M, H] BF16."""
         if isinstance(splits, N.DeviceGroups):
-            with torch.cuda.device(self.w1.device):
+            # (all of it ahead of the update, whose kernel would write a table on another device from this one)
+            _check("x1", x1, _BF16, 2, self.w1.device)
+            _check_groups(splits, x1.shape[0], self.e, x1.device)
+            with torch.cuda.device(x1.device):
                 splits.update()
         h = grouped_gated_w4(self.act, splits, x1, self.w1, self.b1, probs)
         self.ctx = {}  # nothing is kept; MoELayer marks it
