@@ -510,8 +510,9 @@ typedef struct {
 } mgs_grad;
 
 /* norm[0] = the square root of the sum of the squares of all elements of all gradients, summed in FP64 in a fixed order;
- * with clip != 0 also out = grad * min(1, max_norm / (norm + eps)), one rounding to the output's type (the factor is
- * FP32).  A NaN norm makes every output NaN, an infinite one zeros (NaN where the gradient is infinite).
+ * with clip != 0 also out = grad * min(1, max_norm / (norm + eps)): the factor is taken from the FP64 norm and rounded to
+ * FP32, the product is FP32, and a BF16 output rounds that product again.  A NaN norm makes every output NaN, an infinite
+ * gradient zeros (NaN in its own place); a finite norm past FP32's range is returned as infinity and clips like any other.
  * `grads` is a HOST array of `count`; empty gradients may be NULL.  No output may be or overlap another tensor of the
  * call, but for a gradient scaled in place.
  *   workspace  mgs_grad_norm_workspace_bytes() bytes, 8-byte aligned, caller-owned, contents undefined before and

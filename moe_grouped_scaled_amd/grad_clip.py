@@ -80,8 +80,8 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
 
 def clip_grad_norm(grads, max_norm, eps=1e-6, out=None, norm=None, workspace=None, stream=None):
     """Scales `grads` by min(1, max_norm / (norm + eps)), in place or into `out` (contiguous tensors of as many elements,
-    BF16 or FP32), and returns the norm before that.  A NaN norm makes every result NaN, an infinite one zeros (NaN where the
-    gradient is infinite)."""
+    BF16 or FP32), and returns the norm before that.  A NaN norm makes every result NaN, an infinite gradient zeros (NaN in its
+    own place); a finite norm past FP32's range is returned as infinity and clips like any other."""
     grads = list(grads)
     if stream is not None:
         return _on_stream(stream, grads[0] if grads else None, clip_grad_norm, grads, max_norm, eps, out, norm, workspace)
