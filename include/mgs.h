@@ -471,8 +471,9 @@ int64_t mgs_grouped_gated_bwd_workspace_bytes(const mgs_groups* groups, int64_t 
 /* ---- Weights in 4 bits with BF16 rows --------------------------------------------------------------
  * The serving form of the block above: each weight is (q - z) s with a code q in 0 .. 15 and, per group of 32, 64 or
  * 128 elements along k, a BF16 scale s and a zero point z in 0 .. 15 (8 where there are none).  Rows stay in BF16, sums
- * are FP32, no weight is rounded.  Made for few rows per expert (decoding); any number is right.  x is finite: a row with
- * an infinity or NaN gives NaN, in that row only.  n up to 2^20 of any size, k a multiple of the group up to 2^20. */
+ * are FP32, no weight is rounded.  Made for few rows per expert (decoding); any number is right.  x is finite, and so is 31
+ * times the sum of a group's |x| in FP32 (codes are multiplied as 16 + q): a row with an infinity, a NaN or such a sum gives
+ * NaN, in that row only.  n up to 2^20 of any size, k a multiple of the group up to 2^20. */
 
 /* Bytes of packed weights [experts x n x k] (negative MGS_ERR_* on invalid arguments). */
 int64_t mgs_w4_nbytes(int32_t experts, int64_t n, int64_t k, int32_t group, int32_t zeros);
